@@ -187,7 +187,7 @@ def _own(s):
         return awq.w4a16_gemv(s["X"], s["codes"], s["steps"], s["zeros"], bias=s["bias"], gated=case["gated"])
     if op == "experts":
         if "workspace" not in s:  # kept from pass to pass, as a serving loop keeps it
-            s["workspace"] = awq.w4a16_experts_workspace(s["X"].shape[0], s["codes"])
+            s["workspace"] = awq.w4a16_experts_workspace(s["codes"], s["X"].shape[0])
         return awq.w4a16_experts(s["X"], s["offsets"], s["codes"], s["steps"], s["zeros"], gated=case["gated"],
                                  workspace=s["workspace"])
     if op == "dispatch":
