@@ -287,6 +287,87 @@ AWQ_API awq_status awq_w4a16_gemm(const void *X, int64_t M, int64_t K, int64_t l
                                   const float *steps, const float *zeros, int64_t O, void *Y, int64_t ldy,
                                   void *workspace, size_t ws_bytes, awq_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------------
+ * One-token products (W4A16): the deployment GEMM's form for the 1 to 8 tokens of a decode step, in one
+ * launch and without a workspace. Weights, X' and the value of a weight as in awq_w4a16_gemm for few tokens
+ * (the weight enters with its exact value, fp32 sums, one rounding to bf16 at the end).
+ *   gated = 0: Y[m, o] = sum_k X'[m, k] deq(W)[o, k] (+ bias[o]);  Y is [M, O]
+ *   gated = 1: the rows of W are a gate projection's O/2 rows, then an up projection's O/2 rows;
+ *              Y[m, i] = a / (1 + exp(-a)) * b in fp32, a = row i's product, b = row O/2 + i's; Y is [M, O/2]
+ *   X       device bf16 [M, K], row stride ldx (multiple of 8), 16-byte aligned
+ *   codes   device uint32 [O, K/8], 16-byte aligned; steps / zeros device float [O, K/128] (as packed)
+ *   bias    device bf16 [O] or NULL (NULL when gated)
+ *   Y       device bf16, row stride ldy >= its columns (no alignment beyond 2 bytes); must not overlap X
+ * Requires 1 <= M <= AWQ_GEMV_MAX_TOKENS, K % 128 == 0, any O >= 1 (gated: even; at most 8388480 rows, half
+ * of that per projection when gated). Deterministic.
+ * ------------------------------------------------------------------------------------------------- */
+#define AWQ_GEMV_MAX_TOKENS 8
+AWQ_API awq_status awq_w4a16_gemv(const void *X, int64_t M, int64_t K, int64_t ldx, const uint32_t *codes,
+                                  const float *steps, const float *zeros, int64_t O, const void *bias, int gated,
+                                  void *Y, int64_t ldy, awq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------------
+ * Tokens sorted by expert. Slot s = t * top_k + j is the j-th pick of token t; ids holds the expert of every
+ * slot (int32 or int64, id_bytes 4 or 8). An id outside [0, E) names no expert (a padded token, an expert of
+ * another device): its slot has no row.
+ *   offsets  device int32 [E + 1]: first sorted row of each expert; offsets[E] = number of routed slots
+ *   order    device int32 [n_slots]: slot of each sorted row, rows in order of (expert, slot); -1 from
+ *            offsets[E] on
+ *   pos      device int32 [n_slots]: sorted row of each slot, -1 where there is none
+ *   workspace  device, >= awq_expert_sort_workspace_size(n_slots, E) bytes (0 for up to 4096 slots: may be
+ *            NULL then), contents need not be initialised
+ * Requires 1 <= n_slots < 2^31, 1 <= E <= AWQ_MAX_EXPERTS. A token may pick the same expert twice. Stable and
+ * deterministic.
+ * ------------------------------------------------------------------------------------------------- */
+#define AWQ_MAX_EXPERTS 1024
+AWQ_API size_t awq_expert_sort_workspace_size(int64_t n_slots, int64_t E);
+AWQ_API awq_status awq_expert_sort(const void *ids, int id_bytes, int64_t n_slots, int64_t E, void *workspace,
+                                   size_t ws_bytes, int32_t *offsets, int32_t *order, int32_t *pos,
+                                   awq_stream_t stream);
+
+/* Rows in expert order and back. T tokens, top_k picks each; Xs, Ys, dXs, dYs are bf16 [T * top_k, columns] in
+ * sorted rows; matrices as everywhere (16-byte aligned, row strides and columns multiples of 8); offsets,
+ * order and pos from awq_expert_sort. Sums are fp32 in slot order, rounded once to bf16. Rows from offsets[E] on are
+ * neither read nor written. No input may overlap an output.
+ *   awq_expert_gather:           Xs[r] = X[order[r] / top_k]; with scales (device float [E, K], 16-byte aligned)
+ *                                bf16(RN32(X / scales[e])), e the row's expert (the same bits as
+ *                                awq_scale_columns with AWQ_SCALE_DIVIDE)
+ *   awq_expert_gather_backward:  its gradient dX[t] = sum_j RN32(dXs[pos[t, j]] / scales[e]) (scales as there)
+ *   awq_expert_combine:          Y[t] = sum_j weights[t, j] * Ys[pos[t, j]] (weights device float [T, top_k], or
+ *                                NULL for ones); 0 for a token without a row
+ *   awq_expert_combine_backward: its gradients dYs[pos[t, j]] = weights[t, j] * dY[t] (bf16) and
+ *                                dweights[t, j] = <dY[t], Ys[pos[t, j]]> (device float [T, top_k], fp32 sum in a
+ *                                fixed order; 0 where a slot has no row) */
+AWQ_API awq_status awq_expert_gather(const void *X, int64_t T, int64_t K, int64_t ldx, int64_t top_k,
+                                     const int32_t *offsets, int64_t E, const int32_t *order, const float *scales,
+                                     void *Xs, int64_t ldxs, awq_stream_t stream);
+AWQ_API awq_status awq_expert_gather_backward(const void *dXs, int64_t T, int64_t K, int64_t lddxs, int64_t top_k,
+                                              const int32_t *offsets, int64_t E, const int32_t *pos,
+                                              const float *scales, void *dX, int64_t lddx, awq_stream_t stream);
+AWQ_API awq_status awq_expert_combine(const void *Ys, int64_t T, int64_t O, int64_t ldys, int64_t top_k,
+                                      const int32_t *pos, const float *weights, void *Y, int64_t ldy,
+                                      awq_stream_t stream);
+AWQ_API awq_status awq_expert_combine_backward(const void *dY, int64_t T, int64_t O, int64_t lddy, const void *Ys,
+                                               int64_t ldys, int64_t top_k, const int32_t *pos, const float *weights,
+                                               void *dYs, int64_t lddys, float *dweights, awq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------------
+ * Products of the experts (W4A16): Y[r] = Xs[r] deq(W_e)^T for the rows offsets[e] <= r < offsets[e + 1] of
+ * every expert e, or with gated = 1 the gated form of awq_w4a16_gemv.
+ *   Xs      device bf16 [R, K] sorted rows, row stride ldx (multiple of 8)
+ *   codes   device uint32 [E, O, K/8], 16-byte aligned; steps / zeros device float [E, O, K/128]
+ *   Y       device bf16 [R, O] (gated: [R, O/2]), row stride ldy >= its columns; rows from offsets[E] on are left
+ *           as they were; must not overlap Xs
+ *   workspace  device, 16-byte aligned, >= awq_w4a16_experts_workspace_size(R, E, K, O) bytes, ZERO-FILLED
+ *           BEFORE ITS FIRST USE and after a device timeout, which awq_search_status() reports on it
+ * Requires K % 128 == 0, any O >= 1 (gated: even), 1 <= E <= AWQ_MAX_EXPERTS. Deterministic.
+ * ------------------------------------------------------------------------------------------------- */
+AWQ_API size_t awq_w4a16_experts_workspace_size(int64_t R, int64_t E, int64_t K, int64_t O);
+AWQ_API awq_status awq_w4a16_experts(const void *Xs, int64_t R, int64_t K, int64_t ldx, const int32_t *offsets,
+                                     int64_t E, const uint32_t *codes, const float *steps, const float *zeros,
+                                     int64_t O, int gated, void *Y, int64_t ldy, void *workspace, size_t ws_bytes,
+                                     awq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

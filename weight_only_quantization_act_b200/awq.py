@@ -31,6 +31,8 @@ FLAG_SCALES_WEIGHT_AWARE = 0x10
 FLAG_SCALES_RMS = 0x20
 FLAG_QUANT_INT8 = 0x40
 MAX_N_GRID = 64
+GEMV_MAX_TOKENS = 8
+MAX_EXPERTS = 1024
 
 # name -> (restype, argtypes)
 _P, _I64, _I, _U, _SZ, _D = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t,
@@ -58,6 +60,15 @@ SIGNATURES = {
     "awq_scale_rows": (_I, [_P, _I64, _I64, _I64, _P, _I, _P, _I64, _P]),
     "awq_w4a16_workspace_size": (_SZ, [_I64, _I64]),
     "awq_w4a16_gemm": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "awq_w4a16_gemv": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I, _P, _I64, _P]),
+    "awq_expert_sort_workspace_size": (_SZ, [_I64, _I64]),
+    "awq_expert_sort": (_I, [_P, _I, _I64, _I64, _P, _SZ, _P, _P, _P, _P]),
+    "awq_expert_gather": (_I, [_P, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _I64, _P]),
+    "awq_expert_gather_backward": (_I, [_P, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _I64, _P]),
+    "awq_expert_combine": (_I, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P]),
+    "awq_expert_combine_backward": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
+    "awq_w4a16_experts_workspace_size": (_SZ, [_I64, _I64, _I64, _I64]),
+    "awq_w4a16_experts": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _I64, _I, _P, _I64, _P, _SZ, _P]),
 }
 
 
@@ -428,3 +439,277 @@ def w4a16_gemm(X: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, zeros:
                                                 O, _ptr(out), out.stride(0), _ptr(workspace), workspace.numel(),
                                                 _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------------------------------- (8)
+def _on_stream(fn):
+    """Run an entry point on its first tensor argument's device, and on `stream` where one is given: what it
+    allocates then belongs to that stream, so a workspace is not handed to other work while the stream uses it."""
+
+    @functools.wraps(fn)
+    def wrapper(*args, stream=None, **kwargs):
+        first = args[0] if args else next(iter(kwargs.values()))
+        device = first.device if isinstance(first, torch.Tensor) and first.is_cuda else None
+        if stream is not None:
+            if device is not None and stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            with torch.cuda.stream(stream):
+                return fn(*args, **kwargs)
+        if device is None or device.index == torch.cuda.current_device():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(device):
+            return fn(*args, **kwargs)
+
+    return wrapper
+
+
+def _rows(name: str, t: torch.Tensor, device=None) -> torch.Tensor:
+    """A bf16 matrix argument on `device`, with unit column stride."""
+    t = _bf16_matrix(name, t)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride in elements; a single row's stride does not matter and torch may give any number for it."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _tensor(name: str, t: torch.Tensor, dtypes, shape, device) -> torch.Tensor:
+    """A contiguous argument of one of `dtypes`, of this shape, on `device`."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
+    if tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be contiguous, of shape {list(shape)} and on {device}")
+    return t
+
+
+def _rows_out(name: str, out: torch.Tensor | None, rows: int, cols: int, device) -> torch.Tensor:
+    """A bf16 output matrix: a new one, or the caller's."""
+    if out is None:
+        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+    if not isinstance(out, torch.Tensor) or out.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 tensor")
+    if tuple(out.shape) != (rows, cols) or out.device != device or (cols > 1 and out.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}, {cols}] with unit column stride on {device}")
+    return out
+
+
+def _packed(codes, steps, zeros, lead: tuple, K: int, device) -> int:
+    """Checks packed weights [*lead, O, ...] against X's K in-features; returns O."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != len(lead) + 1 + 1:
+        raise TypeError(f"codes must be a {len(lead) + 2}-dimensional int32 tensor, as quantize_pack gives it")
+    O = codes.shape[-2]
+    _tensor("codes", codes, (torch.int32, torch.uint32), (*lead, O, K // 8), device)
+    _tensor("steps", steps, (torch.float32,), (*lead, O, K // 128), device)
+    _tensor("zeros", zeros, (torch.float32,), (*lead, O, K // 128), device)
+    return O
+
+
+@_on_stream
+def w4a16_gemv(X: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, zeros: torch.Tensor,
+               bias: torch.Tensor | None = None, gated: bool = False, out: torch.Tensor | None = None,
+               *, stream=None) -> torch.Tensor:
+    """Y = X' deq(W)^T (+ bias) for 1 to 8 tokens in one launch (bf16 [M, O]). With ``gated`` the rows of W are a
+    gate projection's, then an up projection's, and Y = silu(gate) * up (bf16 [M, O / 2])."""
+    lib = load_library()
+    X = _rows("X", X)
+    M, K = X.shape
+    O = _packed(codes, steps, zeros, (), K, X.device)
+    if bias is not None:
+        _tensor("bias", bias, (torch.bfloat16,), (O,), X.device)
+    out = _rows_out("out", out, M, O // 2 if gated else O, X.device)
+    _check("awq_w4a16_gemv", lib.awq_w4a16_gemv(
+        _ptr(X), M, K, _ld(X), _ptr(codes), _ptr(steps), _ptr(zeros), O, None if bias is None else _ptr(bias),
+        int(gated), _ptr(out), out.stride(0), _stream(None)))
+    return out
+
+
+# --------------------------------------------------------------------------------------------- (9)
+@dataclass
+class ExpertSort:
+    """Where a router's picks ids [T, k] stand in expert order: offsets int32 [E + 1] (first row of each expert),
+    order int32 [T * k] (slot t * k + j of each row, -1 behind the last), pos int32 [T, k] (row of each slot, -1 where
+    an id names no expert)."""
+    offsets: torch.Tensor
+    order: torch.Tensor
+    pos: torch.Tensor
+
+    def checked(self, device) -> tuple:
+        """(T, k, E) after checking the three tensors against each other."""
+        if not isinstance(self.pos, torch.Tensor) or self.pos.dim() != 2 or self.offsets.dim() != 1:
+            raise TypeError("an ExpertSort holds offsets [E + 1], order [T * k] and pos [T, k]")
+        T, k = self.pos.shape
+        E = self.offsets.shape[0] - 1
+        _tensor("pos", self.pos, (torch.int32,), (T, k), device)
+        _tensor("order", self.order, (torch.int32,), (T * k,), device)
+        _tensor("offsets", self.offsets, (torch.int32,), (E + 1,), device)
+        return T, k, E
+
+
+@_on_stream
+def expert_sort(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor | None = None, *, stream=None) -> ExpertSort:
+    """Rows in order of (expert, token, pick) for a router's picks ids [T, k] (int32 or int64). Ids outside
+    [0, n_experts) name no expert."""
+    lib = load_library()
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64) or not ids.is_cuda or ids.dim() != 2:
+        raise TypeError("ids must be a CUDA int32 or int64 matrix [tokens, picks]")
+    ids = ids.contiguous()
+    n = ids.numel()
+    offsets = torch.empty(n_experts + 1 if n_experts >= 0 else 1, dtype=torch.int32, device=ids.device)
+    order = torch.empty(n, dtype=torch.int32, device=ids.device)
+    pos = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+    need = lib.awq_expert_sort_workspace_size(n, n_experts)
+    ws = _workspace(need, ids.device, workspace) if need else None
+    _check("awq_expert_sort", lib.awq_expert_sort(
+        _ptr(ids), ids.element_size(), n, n_experts, _ptr(ws) if need else None, need, _ptr(offsets), _ptr(order),
+        _ptr(pos), _stream(None)))
+    return ExpertSort(offsets, order, pos)
+
+
+def _scales(scales, E: int, K: int, device):
+    return None if scales is None else _ptr(_tensor("scales", scales, (torch.float32,), (E, K), device))
+
+
+@_on_stream
+def expert_gather(X: torch.Tensor, sort: ExpertSort, scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  *, stream=None) -> torch.Tensor:
+    """Token rows in expert order, bf16 [T * k, K]; with ``scales`` (float32 [E, K]) each divided by its expert's AWQ
+    scales, as scale_columns(divide=True) does. Rows behind the last routed one are not written."""
+    lib = load_library()
+    X = _rows("X", X)
+    T, k, E = sort.checked(X.device)
+    K = X.shape[1]
+    if X.shape[0] != T:
+        raise ValueError(f"X has {X.shape[0]} rows, the sort {T} tokens")
+    out = _rows_out("out", out, T * k, K, X.device)
+    _check("awq_expert_gather", lib.awq_expert_gather(
+        _ptr(X), T, K, _ld(X), k, _ptr(sort.offsets), E, _ptr(sort.order), _scales(scales, E, K, X.device), _ptr(out),
+        _ld(out), _stream(None)))
+    return out
+
+
+@_on_stream
+def expert_gather_backward(dXs: torch.Tensor, sort: ExpertSort, scales: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None, *, stream=None) -> torch.Tensor:
+    """Gradient of expert_gather: dX[t] = the sum of its rows of dXs (each divided by its expert's scales)."""
+    lib = load_library()
+    dXs = _rows("dXs", dXs)
+    T, k, E = sort.checked(dXs.device)
+    K = dXs.shape[1]
+    if dXs.shape[0] != T * k:
+        raise ValueError(f"dXs has {dXs.shape[0]} rows, the sort {T * k}")
+    out = _rows_out("out", out, T, K, dXs.device)
+    _check("awq_expert_gather_backward", lib.awq_expert_gather_backward(
+        _ptr(dXs), T, K, _ld(dXs), k, _ptr(sort.offsets), E, _ptr(sort.pos), _scales(scales, E, K, dXs.device),
+        _ptr(out), _ld(out), _stream(None)))
+    return out
+
+
+@_on_stream
+def expert_combine(Ys: torch.Tensor, sort: ExpertSort, weights: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, *, stream=None) -> torch.Tensor:
+    """Y[t] = sum_j weights[t, j] * Ys[pos[t, j]] (bf16 [T, O], fp32 sums; weights float32 [T, k], ones if None)."""
+    lib = load_library()
+    Ys = _rows("Ys", Ys)
+    T, k, _ = sort.checked(Ys.device)
+    O = Ys.shape[1]
+    if Ys.shape[0] != T * k:
+        raise ValueError(f"Ys has {Ys.shape[0]} rows, the sort {T * k}")
+    w = None if weights is None else _ptr(_tensor("weights", weights, (torch.float32,), (T, k), Ys.device))
+    out = _rows_out("out", out, T, O, Ys.device)
+    _check("awq_expert_combine", lib.awq_expert_combine(
+        _ptr(Ys), T, O, _ld(Ys), k, _ptr(sort.pos), w, _ptr(out), _ld(out), _stream(None)))
+    return out
+
+
+@_on_stream
+def expert_combine_backward(dY: torch.Tensor, Ys: torch.Tensor, sort: ExpertSort, weights: torch.Tensor,
+                            out: torch.Tensor | None = None, *, stream=None):
+    """Gradients of expert_combine: (dYs bf16 [T * k, O], dweights float32 [T, k]). ``out`` takes dYs; its rows behind
+    the last routed one are not written."""
+    lib = load_library()
+    dY = _rows("dY", dY)
+    Ys = _rows("Ys", Ys, dY.device)
+    T, k, _ = sort.checked(dY.device)
+    O = dY.shape[1]
+    if dY.shape[0] != T or tuple(Ys.shape) != (T * k, O):
+        raise ValueError(f"dY {list(dY.shape)} and Ys {list(Ys.shape)} do not fit a sort of {T} tokens, {k} picks")
+    _tensor("weights", weights, (torch.float32,), (T, k), dY.device)
+    out = _rows_out("out", out, T * k, O, dY.device)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dY.device)
+    _check("awq_expert_combine_backward", lib.awq_expert_combine_backward(
+        _ptr(dY), T, O, _ld(dY), _ptr(Ys), _ld(Ys), k, _ptr(sort.pos), _ptr(weights), _ptr(out), _ld(out),
+        _ptr(dweights), _stream(None)))
+    return out, dweights
+
+
+# --------------------------------------------------------------------------------------------- (10)
+@_on_stream
+def w4a16_experts_workspace(codes: torch.Tensor, rows: int) -> torch.Tensor:
+    """A zero-filled workspace for w4a16_experts with these codes [E, O, K / 8] and up to `rows` sorted rows."""
+    E, O, words = codes.shape
+    nbytes = load_library().awq_w4a16_experts_workspace_size(rows, E, words * 8, O)
+    return torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=codes.device)
+
+
+@_on_stream
+def w4a16_experts(Xs: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, zeros: torch.Tensor,
+                  gated: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                  *, stream=None) -> torch.Tensor:
+    """Products of sorted rows with their experts' packed weights: Y[r] = Xs[r] deq(W_e)^T for offsets[e] <= r <
+    offsets[e + 1] (codes [E, O, K/8], steps and zeros [E, O, K/128]); ``gated`` as in w4a16_gemv. Rows behind the last
+    routed one are not written."""
+    lib = load_library()
+    Xs = _rows("Xs", Xs)
+    R, K = Xs.shape
+    E = codes.shape[0]
+    O = _packed(codes, steps, zeros, (E,), K, Xs.device)
+    _tensor("offsets", offsets, (torch.int32,), (E + 1,), Xs.device)
+    out = _rows_out("out", out, R, O // 2 if gated else O, Xs.device)
+    if workspace is None:
+        workspace = w4a16_experts_workspace(codes, R)
+    _check("awq_w4a16_experts", lib.awq_w4a16_experts(
+        _ptr(Xs), R, K, _ld(Xs), _ptr(offsets), E, _ptr(codes), _ptr(steps), _ptr(zeros), O, int(gated), _ptr(out),
+        out.stride(0), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(None)))
+    return out
+
+
+@_on_stream
+def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up, down, scales: torch.Tensor | None = None,
+              workspaces=(None, None), out: torch.Tensor | None = None, *, stream=None) -> torch.Tensor:
+    """A feed-forward block of quantized experts: tokens X [T, K] sorted by their picks ids [T, k], divided by each
+    expert's scales, through silu(gate) * up and the down projection of their experts, and back, weighted. gate_up and
+    down are (codes, steps, zeros) of all experts, as quantize_experts gives them."""
+    sort = expert_sort(ids, gate_up[0].shape[0])
+    Xs = expert_gather(X, sort, scales=scales)
+    H = w4a16_experts(Xs, sort.offsets, *gate_up, gated=True, workspace=workspaces[0])
+    Ys = w4a16_experts(H, sort.offsets, *down, workspace=workspaces[1])
+    return expert_combine(Ys, sort, weights=weights, out=out)
+
+
+@_on_stream
+def quantize_experts(X: torch.Tensor, ids: torch.Tensor, W: Sequence[torch.Tensor], n_grid: int = 20, group: int = 128,
+                     *, stream=None):
+    """quantize_layer for every expert of a block, each on the calibration tokens that its router sends there: tokens
+    X [N, K] with picks ids [N, k], W one [O, K] weight (or stacked weights) per expert. Returns scales [E, K] and codes, steps,
+    zeros [E, O, ...], and losses, best_j per expert. An expert without a token is quantized at scales of one (losses NaN,
+    best_j 0). Reads the experts' row counts on the host (one synchronisation)."""
+    E = len(W)
+    mats = [stack_weights(w) for w in W]
+    sort = expert_sort(ids, E)
+    Xs = expert_gather(X, sort)
+    edges = sort.offsets.tolist()
+    parts = []
+    for e, w in enumerate(mats):
+        if edges[e + 1] > edges[e]:
+            parts.append(quantize_layer(Xs[edges[e]:edges[e + 1]], w, n_grid=n_grid, group=group))
+            continue
+        scales = torch.ones(X.shape[1], dtype=torch.float32, device=X.device)
+        codes, steps, zeros = quantize_pack(w, scales, group=group)
+        parts.append(dict(scales=scales, codes=codes, steps=steps, zeros=zeros,
+                          losses=torch.full((n_grid,), float("nan"), dtype=torch.float64, device=X.device),
+                          best_j=torch.zeros(1, dtype=torch.int32, device=X.device)))
+    return {name: torch.stack([p[name] for p in parts])
+            for name in ("scales", "codes", "steps", "zeros", "losses", "best_j")}

@@ -15,6 +15,8 @@
 #include "kernel_loss_gemm.cuh"
 #include "kernel_w4a16.cuh"
 #include "kernel_w4a16_decode.cuh"
+#include "kernel_w4a16_few.cuh"
+#include "kernels_experts.cuh"
 #include "kernels_simple.cuh"
 
 namespace {
@@ -143,6 +145,10 @@ awq_status device_info(DeviceInfo** out) {
                                   awq::dec::Shape<48>::SMEM));
     AWQ_CUDA(cudaFuncSetAttribute(awq::dec::w4a16_decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   awq::dec::Shape<64>::SMEM));
+    AWQ_CUDA(cudaFuncSetAttribute(awq::few::w4a16_few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  awq::few::SMEM_MAX));
+    AWQ_CUDA(cudaFuncSetAttribute(awq::few::w4a16_few_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  awq::few::SMEM_MAX));
     d.gemm_attr_set = true;
   }
   *out = &d;
@@ -958,3 +964,5 @@ extern "C" awq_status awq_w4a16_gemm(const void* X, int64_t M, int64_t K, int64_
   AWQ_TRY(check_launch("w4a16_gemm_kernel"));
   return ok();
 }
+
+#include "capi_experts.cuh"

@@ -1,0 +1,304 @@
+// kernels_experts.cuh - tokens sorted by expert and back: the counting sort of a router's picks, the gather
+// of token rows into expert order (optionally divided by each expert's scales), the weighted sum back per
+// token, and the gradients of both.
+//
+// A slot s = t * top_k + j is the j-th pick of token t. order[r] is the slot of sorted row r, pos[s] the row of
+// slot s, -1 where a pick names no expert. Every kernel checks the index that it loads against the array
+// that it indexes, so whatever stands in order, pos or offsets no access leaves the arguments.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+
+namespace awq {
+namespace ex {
+
+constexpr int SORT_THREADS = 256;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_ITERS = 16;                                   // slots per lane and tile
+constexpr int SORT_TILE = SORT_THREADS * SORT_ITERS;             // 4096 slots: one CTA sorts these alone
+constexpr int MAX_EXPERTS = 1024;
+constexpr int SORT_MAX_BLOCKS = 256;
+
+template <typename ID>
+__device__ __forceinline__ int expert_of(const ID* ids, int64_t s, int64_t n, int E) {
+  if (s >= n) return -1;
+  const ID v = ids[s];
+  return v >= 0 && v < static_cast<ID>(E) ? static_cast<int>(v) : -1;
+}
+
+// counts[b][e]: picks of expert e among block b's slots.
+template <typename ID>
+__global__ void __launch_bounds__(SORT_THREADS) expert_count_kernel(const ID* __restrict__ ids, int64_t n, int E,
+                                                                    int64_t per_block, int* __restrict__ counts) {
+  __shared__ int hist[MAX_EXPERTS];
+  for (int e = threadIdx.x; e < E; e += SORT_THREADS) hist[e] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * per_block, end = min(begin + per_block, n);
+  for (int64_t s = begin + threadIdx.x; s < end; s += SORT_THREADS) {
+    const int e = expert_of(ids, s, n, E);
+    if (e >= 0) atomicAdd(&hist[e], 1);  // a count: the order of the additions does not show
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += SORT_THREADS) counts[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
+}
+
+// Exclusive prefix sum of v[0..E-1] in place by the whole block (E <= 4 * SORT_THREADS); returns the total.
+__device__ __forceinline__ int block_scan(int* v, int E, int* warp_sums) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int x[4], mine = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = threadIdx.x * 4 + i;
+    x[i] = e < E ? v[e] : 0;
+    mine += x[i];
+  }
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int before = inc - mine, all = 0;
+  for (int w = 0; w < SORT_WARPS; ++w) {
+    if (w < warp) before += warp_sums[w];
+    all += warp_sums[w];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = threadIdx.x * 4 + i;
+    if (e < E) v[e] = before;
+    before += x[i];
+  }
+  __syncthreads();
+  return all;
+}
+
+// Stable counting sort. Block b places its slots; with counts == nullptr there is one block, which counts
+// for itself. Inside a block the slots are taken in tiles of 4096; each warp takes 512 consecutive slots of
+// the tile, 32 at a time, and a lane's rank among equal picks is the popcount of the match mask below it
+// plus the warp's running count, so equal picks keep the order of their slots.
+template <typename ID>
+__global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const ID* __restrict__ ids, int64_t n, int E,
+                                                                    int64_t per_block, const int* __restrict__ counts,
+                                                                    int* __restrict__ offsets, int* __restrict__ order,
+                                                                    int* __restrict__ pos) {
+  extern __shared__ int sort_smem[];
+  int* base = sort_smem;               // [E] next row of each expert for this block
+  int* whist = sort_smem + E;          // [SORT_WARPS][E]
+  __shared__ int warp_sums[SORT_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t begin = blockIdx.x * per_block, end = min(begin + per_block, n);
+
+  int before[MAX_EXPERTS / SORT_THREADS];
+  if (counts != nullptr) {
+#pragma unroll
+    for (int i = 0; i < MAX_EXPERTS / SORT_THREADS; ++i) {
+      const int e = threadIdx.x + i * SORT_THREADS;
+      before[i] = 0;
+      if (e < E) {
+        int all = 0;
+        for (unsigned b = 0; b < gridDim.x; ++b) {
+          const int c = counts[static_cast<int64_t>(b) * E + e];
+          if (b < blockIdx.x) before[i] += c;
+          all += c;
+        }
+        base[e] = all;
+      }
+    }
+  } else {
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) base[e] = 0;
+    __syncthreads();
+    for (int64_t s = begin + threadIdx.x; s < end; s += SORT_THREADS) {
+      const int e = expert_of(ids, s, n, E);
+      if (e >= 0) atomicAdd(&base[e], 1);
+    }
+  }
+  __syncthreads();
+  const int routed = block_scan(base, E, warp_sums);
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) offsets[e] = base[e];
+    if (threadIdx.x == 0) offsets[E] = routed;
+    __syncthreads();
+  }
+  if (counts != nullptr) {
+#pragma unroll
+    for (int i = 0; i < MAX_EXPERTS / SORT_THREADS; ++i) {
+      const int e = threadIdx.x + i * SORT_THREADS;
+      if (e < E) base[e] += before[i];
+    }
+    __syncthreads();
+  }
+
+  for (int64_t tile = begin; tile < end; tile += SORT_TILE) {
+    for (int i = threadIdx.x; i < SORT_WARPS * E; i += SORT_THREADS) whist[i] = 0;
+    __syncthreads();
+    int* mine = whist + warp * E;
+    int ranks[SORT_ITERS], picks[SORT_ITERS];
+    const int64_t s0 = tile + warp * 32 * SORT_ITERS + lane;
+#pragma unroll
+    for (int i = 0; i < SORT_ITERS; ++i) {
+      const int64_t s = s0 + i * 32;
+      const int e = expert_of(ids, s, end, E);
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const int below = __popc(same & ((1u << lane) - 1u));
+      picks[i] = e;
+      ranks[i] = e >= 0 ? mine[e] + below : 0;
+      __syncwarp();
+      if (e >= 0 && below == 0) mine[e] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // each warp's first row of each expert; the next tile starts behind this one
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
+      int at = base[e];
+#pragma unroll
+      for (int w = 0; w < SORT_WARPS; ++w) {
+        const int c = whist[w * E + e];
+        whist[w * E + e] = at;
+        at += c;
+      }
+      base[e] = at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SORT_ITERS; ++i) {
+      const int64_t s = s0 + i * 32;
+      if (s < end) {
+        const int row = picks[i] >= 0 ? mine[picks[i]] + ranks[i] : -1;
+        pos[s] = row;
+        if (row >= 0) order[row] = static_cast<int>(s);
+        if (s >= routed) order[s] = -1;  // rows behind the last: no slot writes them
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ rows
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  f[4] = __uint_as_float(v.z << 16); f[5] = __uint_as_float(v.z & 0xFFFF0000u);
+  f[6] = __uint_as_float(v.w << 16); f[7] = __uint_as_float(v.w & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    r[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// The expert whose rows hold `row`: the last e with offsets[e] <= row.
+__device__ __forceinline__ int expert_of_row(const int* __restrict__ offsets, int E, int row) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (offsets[mid] <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+constexpr int ROW_THREADS = 256;
+
+// Xs[r] = X[order[r] / top_k] (/ scales[expert of r]): one row per block, 16 bytes per thread and step.
+__global__ void __launch_bounds__(ROW_THREADS) expert_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t T,
+                                                                    int64_t K, const int* __restrict__ offsets, int E,
+                                                                    const int* __restrict__ order, int top_k,
+                                                                    const float* __restrict__ scales,
+                                                                    uint16_t* __restrict__ Xs, int64_t ldxs) {
+  const int64_t r = blockIdx.x;
+  const int slot = order[r];
+  if (slot < 0 || slot >= T * top_k) return;
+  const uint4* src = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(slot / top_k) * ldx);
+  uint4* dst = reinterpret_cast<uint4*>(Xs + r * ldxs);
+  const float* sc = scales == nullptr ? nullptr : scales + expert_of_row(offsets, E, static_cast<int>(r)) * K;
+  for (int64_t c = threadIdx.x; c < K / 8; c += ROW_THREADS) {
+    uint4 v = src[c];
+    if (sc != nullptr) {
+      float f[8];
+      unpack8(v, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], sc[c * 8 + i]);
+      v = pack8(f);
+    }
+    dst[c] = v;
+  }
+}
+
+// Y[t] = sum over token t's routed slots, in slot order, of weight * Ys[pos] (or Ys[pos] / scales[expert]), in fp32.
+__global__ void __launch_bounds__(ROW_THREADS) expert_combine_kernel(const uint16_t* __restrict__ Ys, int64_t ldys, int64_t K,
+                                                                     const int* __restrict__ pos, int top_k, int64_t n_rows,
+                                                                     const float* __restrict__ weights,
+                                                                     const int* __restrict__ offsets, int E,
+                                                                     const float* __restrict__ scales,
+                                                                     uint16_t* __restrict__ Y, int64_t ldy) {
+  const int64_t t = blockIdx.x;
+  for (int64_t c = threadIdx.x; c < K / 8; c += ROW_THREADS) {
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < top_k; ++j) {
+      const int64_t s = t * top_k + j;
+      const int row = pos[s];
+      if (row < 0 || row >= n_rows) continue;
+      float f[8];
+      unpack8(*reinterpret_cast<const uint4*>(Ys + row * ldys + c * 8), f);
+      if (scales != nullptr) {
+        const float* sc = scales + expert_of_row(offsets, E, row) * K + c * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += __fdiv_rn(f[i], sc[i]);
+      } else {
+        const float w = weights == nullptr ? 1.0f : weights[s];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      }
+    }
+    *reinterpret_cast<uint4*>(Y + t * ldy + c * 8) = pack8(acc);
+  }
+}
+
+// dYs[pos] = weight * dY[t], dweights = <dY[t], Ys[pos]> in fp32 (fixed order: a thread's columns in order, then
+// the warp's butterfly, then the warps in order), 0 for slots without a row. One block per slot.
+__global__ void __launch_bounds__(ROW_THREADS) expert_combine_backward_kernel(
+    const uint16_t* __restrict__ dY, int64_t lddy, const uint16_t* __restrict__ Ys, int64_t ldys, int64_t K,
+    const int* __restrict__ pos, int top_k, int64_t n_rows, const float* __restrict__ weights, uint16_t* __restrict__ dYs,
+    int64_t lddys, float* __restrict__ dweights) {
+  __shared__ float sums[ROW_THREADS / 32];
+  const int64_t s = blockIdx.x, t = s / top_k;
+  const int row = pos[s];
+  if (row < 0 || row >= n_rows) {
+    if (threadIdx.x == 0) dweights[s] = 0.0f;
+    return;
+  }
+  const float w = weights[s];
+  float dot = 0.0f;
+  for (int64_t c = threadIdx.x; c < K / 8; c += ROW_THREADS) {
+    float g[8], y[8];
+    unpack8(*reinterpret_cast<const uint4*>(dY + t * lddy + c * 8), g);
+    unpack8(*reinterpret_cast<const uint4*>(Ys + row * ldys + c * 8), y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dot = fmaf(g[i], y[i], dot);
+      g[i] *= w;
+    }
+    *reinterpret_cast<uint4*>(dYs + row * lddys + c * 8) = pack8(g);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = dot;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v = 0.0f;
+    for (int i = 0; i < ROW_THREADS / 32; ++i) v += sums[i];
+    dweights[s] = v;
+  }
+}
+
+}  // namespace ex
+}  // namespace awq
