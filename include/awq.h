@@ -353,7 +353,8 @@ AWQ_API awq_status awq_expert_combine_backward(const void *dY, int64_t T, int64_
 
 /* ---------------------------------------------------------------------------------------------------
  * Products of the experts (W4A16): Y[r] = Xs[r] deq(W_e)^T for the rows offsets[e] <= r < offsets[e + 1] of
- * every expert e, or with gated = 1 the gated form of awq_w4a16_gemv.
+ * every expert e, or with gated = 1 the gated form of awq_w4a16_gemv. An expert of up to 64 rows gets the exact
+ * value of its weights, one of more rows bf16(RN32(RN32(q - z) * step)), as in awq_w4a16_gemm.
  *   Xs      device bf16 [R, K] sorted rows, row stride ldx (multiple of 8)
  *   codes   device uint32 [E, O, K/8], 16-byte aligned; steps / zeros device float [E, O, K/128]
  *   Y       device bf16 [R, O] (gated: [R, O/2]), row stride ldy >= its columns; rows from offsets[E] on are left

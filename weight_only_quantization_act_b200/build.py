@@ -23,7 +23,7 @@ LIB = os.path.join(LIB_DIR, "libawq.so")
 SOURCES = ["awq_capi.cu"]
 HEADERS = ["ptx.cuh", "numerics.cuh", "kernels_simple.cuh", "kernel_loss_gemm.cuh", "kernel_w4a16.cuh",
            "kernel_w4a16_decode.cuh", "dequant_w4.cuh", "kernel_w4a16_few.cuh", "kernels_experts.cuh",
-           "capi_experts.cuh"]
+           "kernel_w4a16_experts.cuh", "capi_experts.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

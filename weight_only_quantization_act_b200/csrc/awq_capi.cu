@@ -15,6 +15,7 @@
 #include "kernel_loss_gemm.cuh"
 #include "kernel_w4a16.cuh"
 #include "kernel_w4a16_decode.cuh"
+#include "kernel_w4a16_experts.cuh"
 #include "kernel_w4a16_few.cuh"
 #include "kernels_experts.cuh"
 #include "kernels_simple.cuh"
@@ -52,6 +53,7 @@ struct DeviceInfo {
   bool gemm_attr_set = false;
   int gemm_clusters = 0;  // CTA pairs of the loss GEMM that fit on the device at once
   int w4_clusters = 0;    // CTA pairs of the W4A16 GEMM that fit on the device at once
+  int expert_clusters = 0;  // CTA pairs of the experts' GEMM that fit on the device at once
 };
 
 constexpr int kMaxDevices = 64;
@@ -149,6 +151,14 @@ awq_status device_info(DeviceInfo** out) {
                                   awq::few::SMEM_MAX));
     AWQ_CUDA(cudaFuncSetAttribute(awq::few::w4a16_few_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   awq::few::SMEM_MAX));
+    AWQ_CUDA(cudaFuncSetAttribute(awq::grp::w4a16_experts_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  awq::grp::SMEM_BYTES));
+    AWQ_CUDA(cudaFuncSetAttribute(awq::grp::w4a16_experts_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  awq::grp::SMEM_BYTES));
+    cfg.blockDim = dim3(awq::grp::THREADS);
+    cfg.dynamicSmemBytes = awq::grp::SMEM_BYTES;
+    AWQ_CUDA(cudaOccupancyMaxActiveClusters(&d.expert_clusters, awq::grp::w4a16_experts_kernel<true>, &cfg));
+    if (d.expert_clusters < 1) return fail(AWQ_ERR_UNSUPPORTED, "the experts' GEMM does not fit on this device");
     d.gemm_attr_set = true;
   }
   *out = &d;
@@ -201,7 +211,8 @@ awq_status make_tmap_plain(CUtensorMap* map, const void* base, CUtensorMapDataTy
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Code words [rows][cols] (uint32) in boxes of 32 words x box_rows with 128-byte swizzle.
+// Code words [rows][cols] (uint32) in boxes of 32 words x box_rows with 128-byte swizzle (words past a row's end
+// arrive as zeros).
 awq_status make_tmap_codes_sw128(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr) return fail(AWQ_ERR_CUDA, "cuTensorMapEncodeTiled not available from the driver");

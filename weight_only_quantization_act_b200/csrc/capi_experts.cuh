@@ -243,6 +243,10 @@ extern "C" awq_status awq_expert_combine_backward(const void* dY, int64_t T, int
 }
 
 // --------------------------------------------------------------------------------------- experts' products
+namespace {
+constexpr int kFewRows = 64;  // experts with up to this many rows run the few-token kernel
+}
+
 extern "C" size_t awq_w4a16_experts_workspace_size(int64_t R, int64_t E, int64_t K, int64_t O) {
   if (R < 1 || E < 1 || E > AWQ_MAX_EXPERTS || K < 128 || O < 1) return 0;
   return 512;  // status word
@@ -276,7 +280,38 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   p.O = O;
   p.K = K;
   p.G = K / 128;
-  p.max_rows = 0x7fffffff;
+  p.max_rows = kFewRows;
   AWQ_TRY(launch_few(p, E, std::min(E, R), R, gated != 0, d->sms, st));
+  if (R <= kFewRows) return ok();
+
+  const int64_t tile_out = gated ? awq::grp::HALF : 2 * awq::grp::HALF;
+  const int64_t n_bands = ((gated ? O / 2 : O) + tile_out - 1) / tile_out;
+  if (E * O >= (1ll << 31) || (R / awq::grp::BN + E) * n_bands >= (1ll << 31))
+    return fail(AWQ_ERR_INVALID_ARG, "too many weight rows or tiles");
+  CUtensorMap tmX, tmC;
+  AWQ_TRY(make_tmap(&tmX, Xs, R, K, ldx, awq::grp::X_BOX));
+  AWQ_TRY(make_tmap_codes_sw128(&tmC, codes, E * O, K / 8, gated ? 16 : awq::grp::HALF));
+  awq::grp::Params q = {};
+  q.offsets = offsets;
+  q.steps = steps;
+  q.zeros = zeros;
+  q.Y = static_cast<uint16_t*>(Y);
+  q.R = R;
+  q.O = O;
+  q.G = K / 128;
+  q.ldy = ldy;
+  q.E = static_cast<int>(E);
+  q.min_rows = kFewRows + 1;
+  q.n_bands = static_cast<int>(n_bands);
+  q.num_kb = static_cast<int>(K / awq::grp::BK);
+  q.pair_params = p.pair_params;
+  q.status = static_cast<awq::DeviceStatus*>(workspace);
+  q.limit_ns = g_wait_limit_ns.load();
+  const unsigned ctas = static_cast<unsigned>(2 * d->expert_clusters);
+  if (gated)
+    awq::grp::w4a16_experts_kernel<true><<<ctas, awq::grp::THREADS, awq::grp::SMEM_BYTES, st>>>(tmX, tmC, q);
+  else
+    awq::grp::w4a16_experts_kernel<false><<<ctas, awq::grp::THREADS, awq::grp::SMEM_BYTES, st>>>(tmX, tmC, q);
+  AWQ_TRY(check_launch("w4a16_experts_kernel"));
   return ok();
 }
