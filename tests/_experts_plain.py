@@ -31,25 +31,26 @@ def dequantized(codes, steps, zeros):
     return torch.from_numpy((q - z) * s)
 
 
-def product(X, codes, steps, zeros, exact_weights=True):
+def product(X, codes, steps, zeros, rounded_far_zeros=False):
     """(X deq(W)^T in 64 bits, bound on a kernel's fp32 error before its output rounding).
 
-    Exact weights, per group g (A_g = sum of |x| over it): S_g is 128 additions of terms up to 143 |x|, each off by
-    at most one unit 2^-23 (the tensor cores may truncate); Sx_g 128 additions in fp32 and its product with 128 + z;
-    the difference and the product with the step one rounding each of values up to (15 + |z|) A_g; the running sums
-    over G groups and up to 8 slices another G + 8 of them.
-    bf16 weights: each weight off by half a bf16 step (2^-8 relative), and K / 16 + 16 fp32 additions of one unit."""
+    Per group g (A_g = sum of |x| over it): S_g is 128 additions of terms up to 143 |x|, each off by at most one unit
+    2^-23 (the tensor cores may truncate); Sx_g 128 additions in fp32 and its product with 128 + z; the difference and
+    the product with the step one rounding each of values up to (15 + |z|) A_g; the running sums over G groups and
+    up to 8 slices another G + 8 of them. (A kernel that sums q - z itself stays below the same bound.)
+    rounded_far_zeros: q - z enters rounded to bf16, which is exact up to 256; where |z| > 240 a weight is then off by
+    half a bf16 step, 2^-8 of its size."""
     x = X.double()
     W = dequantized(codes, steps, zeros)
     G = steps.shape[1]
-    if exact_weights:
-        A = x.abs().view(x.shape[0], G, GROUP).sum(2)
-        z = zeros.double().abs()
-        coef = steps.double() * (2 * 128 * 143 + 130 * (128 + z) + (G + 12) * (15 + z))
-        return x @ W.T, 2.0 ** -24 * (A @ coef.T)
-    # the dequantized value is rounded to fp32 (twice at most) and then to bf16
-    size = x.abs() @ W.abs().T
-    return x @ W.T, (2.0 ** -8 + 2.0 ** -22 + (x.shape[1] / 16 + 16) * 2.0 ** -23) * size
+    A = x.abs().view(x.shape[0], G, GROUP).sum(2)
+    z = zeros.double().abs()
+    coef = steps.double() * (2 * 128 * 143 + 130 * (128 + z) + (G + 12) * (15 + z))
+    err = 2.0 ** -24 * (A @ coef.T)
+    if rounded_far_zeros:
+        far = (z > 240).repeat_interleave(GROUP, 1)
+        err = err + 2.0 ** -8 * (x.abs() @ (W.abs() * far).T)
+    return x @ W.T, err
 
 
 def gate(P, err):

@@ -211,14 +211,15 @@ def offsets_of(counts):
     return torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32)
 
 
-def check_experts(Xs, counts, parts, got, gated, exact_rows=64):
-    """Each expert's rows against 64 bits; an expert with more than exact_rows rows may take bf16 weights."""
+FEW_ROWS = 16  # the weights of an expert with more rows enter as q - z in bf16
+
+
+def check_experts(Xs, counts, parts, got, gated):
+    """Each expert's rows against 64 bits."""
     edges = offsets_of(counts).tolist()
     for e, (a, b) in enumerate(zip(edges, edges[1:])):
         if b > a:
-            ref, err = plain.product(Xs[a:b], *parts[e], exact_weights=True)
-            if b - a > exact_rows:
-                err = torch.maximum(err, plain.product(Xs[a:b], *parts[e], exact_weights=False)[1])
+            ref, err = plain.product(Xs[a:b], *parts[e], rounded_far_zeros=b - a > FEW_ROWS)
             plain.assert_within(got[a:b], *(plain.gate(ref, err) if gated else (ref, err)))
 
 
@@ -327,8 +328,8 @@ def moe_plain(X, ids, weights, gate_up, down, scales):
 
 @pytest.mark.parametrize("T", [1, 6, 700])
 def test_block_of_experts(T):
-    """Sort, gather, gated products, down products and combine together: the same bits as the calls one by one, and within
-    four bf16 roundings (input, gate, down, sum; bf16 weights in both products) of 64 bits in the 2-norm."""
+    """Sort, gather, gated products, down products and combine together: the same bits as the calls one by one, and within the
+    four bf16 roundings between the products of 64 bits in the 2-norm."""
     E, k, K, I = 5, 2, 512, 384
     X = normal((T, K), 50)
     ids = picks(T, k, E, 51, unrouted=0.05)
@@ -349,8 +350,9 @@ def test_block_of_experts(T):
     side.synchronize()
     assert torch.equal(other, got)
     ref = moe_plain(X, ids, weights, gp, dp, scales)
-    # half steps of the six roundings that act on the result, the gate's counted twice (it multiplies two products)
-    assert float((got.cpu().double() - ref).norm()) <= 8 * 2.0 ** -8 * float(ref.norm()) + 1e-30
+    # half steps of the roundings that act on the result: the input's twice (the gate multiplies two products of it),
+    # the gate's, the down product's and the sum's
+    assert float((got.cpu().double() - ref).norm()) <= 5 * 2.0 ** -8 * float(ref.norm()) + 1e-30
 
 
 def test_quantize_experts_matches_each_layer():

@@ -1,29 +1,38 @@
 // kernel_w4a16_experts.cuh - products of many rows with their experts' packed 4-bit weights: Y[r] = X'[r] deq(W_e)^T
 // for the sorted rows of each expert, optionally with the SiLU gate of a stacked gate and up projection in the
-// epilogue. deq(W)[o, k] = bf16(RN32(RN32(q - z) * step)), as in the many-token kernel of w4a16_gemm; an expert with few
-// rows is left to kernel_w4a16_few.cuh.
+// epilogue. An expert with few rows is left to kernel_w4a16_few.cuh.
 //
-// The weights stand on the MMA's M side and the expert's tokens on its N side, whose width is set per tile: a tile
-// is 256 weight rows (128 per CTA of a pair; gated: 128 outputs, their gate and up rows in turns of 16) times up to
-// 256 tokens of one expert, N the tokens rounded up to 16, so a ragged expert wastes less than 16 columns of tensor
-// work. Experts of more than 256 rows are cut into tiles of nearly equal width. A row of the accumulator is a weight
-// row, so its lanes store consecutive outputs of one token and no store goes past an expert's last row.
+// Mathematics: Y[m, o] = sum_g step[o, g] sum_{k in g} (q[o, k] - z[o, g]) x'[m, k]. The tensor cores sum a group's
+// q - z, exact in bf16, into a fresh fp32 accumulator; the epilogue warps scale each group by its fp32 step and add
+// it to fp32 sums in registers. So the weight enters with its exact value (a zero point beyond +-240, which
+// takes a group of nearly equal weights, leaves q - z rounded to bf16: the rounding that a restored bf16 weight
+// has everywhere), and a code costs less than its dequantization: two masks per word split it into even and odd
+// nibbles, a byte permute puts a byte of each under a zero byte (the byte's copied sign), which is the bf16
+// subnormal q 2^-133 or 16 q 2^-133, and one paired bf16 FMA gives (q - z) 2^-6 for two in-features in their natural
+// order. The 2^6 goes into the step.
 //
-// Bounds: at N = 256 a k-block of 64 in-features takes the tensor cores 512 cycles and the dequantization about
-// 205 issue cycles of every SM quarter; below N = 100 the dequantization is the longer one, and it then consumes packed weights
-// at about the rate that HBM delivers them (4 KB per SM in 205 cycles).
+// The weights stand on the MMA's M side, read from tensor memory, and the expert's tokens on its N side, whose
+// width is set per tile: a tile is 256 weight rows (128 per CTA of a pair; gated: 128 outputs, their gate and up rows
+// in turns of 16) times up to 192 tokens of one expert, N the tokens rounded up to 16, so a ragged expert wastes less
+// than 16 columns of tensor work. Experts of more than 192 rows are cut into tiles of nearly equal width. A row of
+// the accumulator is a weight row, so its lanes store consecutive outputs of one token and no store goes past an
+// expert's last row.
+//
+// Bounds: at N = 192 a group takes the tensor cores 768 cycles, the unpacking about 200 and the scaling about 140
+// issue cycles of every SM quarter. Below N = 60 the codes arrive no faster than that from HBM (9 KB per SM and
+// group). 192 and not 256 tokens: two accumulators of N columns and four operand buffers of 32 fill tensor memory.
 //
 // Persistent, clusters of 2 CTAs, one CTA per SM; every CTA makes the table of tiles from the row offsets for
 // itself and takes each n-th tile, so nothing is exchanged between pairs. Warps of a CTA:
-//   0      TMA of this CTA's half of the tile's token rows (boxes of 32 rows x 64 in-features, 128-byte swizzle),
-//          counted on the even CTA's barrier
-//   1      tensor memory; the even CTA issues the pair MMAs (cta_group::2, M = 256, N, K = 16) into two
-//          256-column accumulators in turn, so the epilogue of a tile overlaps the next one
-//   2-5    epilogue
-//   6      TMA of the code words, 128 rows x 256 in-features at a time (128 bytes of a row), into a ring of its own
-//   7      steps and zero points of those rows and groups by cp.async, counted on the same barrier
-//   8-23   dequantizers: warps 8 + 4 s .. 11 + 4 s fill operand stage s, a weight row per lane, and hold the result
-//          in registers until the stage is free
+//   0      TMA of this CTA's half of the tile's token rows (boxes of 32 rows x 64 in-features, 128-byte swizzle)
+//          into a ring of 8, counted on the even CTA's barrier
+//   1      tensor memory; the even CTA issues the pair MMAs (cta_group::2, M = 256, N, K = 16, A from tensor memory)
+//          into two accumulators in turn, one group each
+//   2      TMA of the code words, 128 rows x 256 in-features at a time (128 bytes of a row), into a ring of its own
+//   3      steps and zero points of those rows and groups by cp.async, counted on the same barrier
+//   4-11   scaling and epilogue: two warps per quarter of the rows, alternate blocks of 16 tokens
+//   12-19  unpackers: two sets of four warps on alternate k-blocks of 64 in-features, a weight row per lane, into
+//          four operand buffers
 // Every wait is bounded.
 #pragma once
 #include <cstdint>
@@ -38,31 +47,38 @@
 namespace awq {
 namespace grp {
 
-constexpr int HALF = 128;                         // weight rows per CTA, and token rows per CTA at most
-constexpr int BN = 256;                           // tokens per tile at most
+constexpr int HALF = 128;                         // weight rows per CTA
+constexpr int BN = 192;                           // tokens per tile at most
 constexpr int BK = 64;
 constexpr int UK = 16;
-constexpr int STAGES = 4;
-constexpr int A_BYTES = HALF * BK * 2;            // 16 KB  dequantized weight rows
-constexpr int X_BYTES = HALF * BK * 2;            // 16 KB  token rows
-constexpr int STAGE_BYTES = A_BYTES + X_BYTES;
+constexpr int XSTAGES = 8;                        // token ring
 constexpr int X_BOX = 32;                         // token rows per TMA box
 constexpr int X_BOX_BYTES = X_BOX * BK * 2;
+constexpr int X_BYTES = BN / 2 * BK * 2;          // 12 KB  this CTA's token rows
+constexpr int ASTAGES = 4;                        // operand buffers in tensor memory
+constexpr int A_COLS = BK / 2;                    // two in-features per 32-bit column
 constexpr int CSTAGES = 4;                        // code ring
 constexpr int SLOT_KB = 4;                        // k-blocks per code slot: 32 words = 128 bytes of each row
 constexpr int C_BYTES = HALF * 128;               // 16 KB  code words
 constexpr int P_BYTES = HALF * 2 * 4;             // 1 KB   steps (zero points) of two groups
 constexpr int CSTAGE_BYTES = C_BYTES + 2 * P_BYTES;
-constexpr int DQ_WARPS = 4 * STAGES;
-constexpr int FIRST_DQ = 8;
+constexpr int FIRST_EPI = 4, EPI_WARPS = 8;
+constexpr int FIRST_DQ = 12, DQ_SETS = 2, DQ_WARPS = 4 * DQ_SETS;
 constexpr int THREADS = 32 * (FIRST_DQ + DQ_WARPS);
+// 640 threads x 96 registers at launch; the scaling warps hold 96 sums each
+constexpr int LAUNCH_REGS = 96, EPI_REGS = 152, OTHER_REGS = 56;
+static_assert(32 * (EPI_WARPS * EPI_REGS + (THREADS / 32 - EPI_WARPS) * OTHER_REGS) <= THREADS * LAUNCH_REGS,
+              "the shares fit what the block was launched with");
+constexpr int CHUNKS = BN / 16 / 2;               // blocks of 16 tokens per scaling warp
 constexpr int MAX_EXPERTS = 1024;
 constexpr int TABLE_BYTES = 2 * (MAX_EXPERTS + 1) * 4;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + CSTAGES * CSTAGE_BYTES + TABLE_BYTES + 1024;
+constexpr int SMEM_BYTES = XSTAGES * X_BYTES + CSTAGES * CSTAGE_BYTES + TABLE_BYTES + 1024;
 constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t A_COL0 = 2 * BN;
+static_assert(A_COL0 + ASTAGES * A_COLS <= TMEM_COLS, "accumulators and operand buffers fit tensor memory");
 static_assert(SMEM_BYTES <= 232448, "fits the 227 KB of dynamic shared memory");
-static_assert(STAGE_BYTES % 1024 == 0 && CSTAGE_BYTES % 1024 == 0, "tiles stay 1024-byte aligned");
-static_assert(SLOT_KB == STAGES, "each set of dequantizers has at most one k-block of a code slot");
+static_assert(X_BYTES % 1024 == 0 && CSTAGE_BYTES % 1024 == 0 && X_BYTES % X_BOX_BYTES == 0,
+              "tiles stay 1024-byte aligned and whole boxes fit");
 
 struct Params {
   const int* offsets;      // [E + 1]
@@ -88,7 +104,7 @@ __device__ __forceinline__ int token_tiles(int rows) { return (rows + BN - 1) / 
 // Rows per token tile: nearly equal tiles, full ones where there are so many that rounding up to 16 could
 // leave the last one empty.
 __device__ __forceinline__ int tile_rows(int rows, int tiles) {
-  return tiles >= 16 ? BN : ((rows + tiles - 1) / tiles + 15) & ~15;
+  return tiles >= BN / 16 ? BN : ((rows + tiles - 1) / tiles + 15) & ~15;
 }
 
 __device__ __forceinline__ Tile tile_of(int t, const int* first_tile, const int* first_row, int E) {
@@ -114,44 +130,94 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Pair MMA with A from tensor memory (each CTA's 128 rows in its own), B half from each CTA's shared memory.
+__device__ __forceinline__ void umma_bf16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                  uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// y += s * v on both fp32 lanes, v given as two registers.
+__device__ __forceinline__ void fma_f32x2(uint64_t& y, uint64_t s, uint32_t lo, uint32_t hi) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(y) : "l"(f32x2_pack(lo, hi)), "l"(s));
+}
+
+// (q - z) 2^-6 of the word's eight codes, two per register in the order of the in-features. `zb`: -z 2^-6 in both
+// halves; exact for |z| <= 240.
+__device__ __forceinline__ void unpack_word(uint32_t w, uint32_t zb, uint32_t* o) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = w & 0xF0F0F0F0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // bytes: even_j, its sign (0), odd_j, the sign of even_j (0)
+    const uint32_t sel = (8u | j) << 12 | (4u | j) << 8 | (8u | j) << 4 | j;
+    uint32_t t;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(t) : "r"(even), "r"(odd), "r"(sel));
+    // low half q 2^-133 * 2^127, high half 16 q 2^-133 * 2^123
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[j]) : "r"(t), "r"(0x7D007F00u), "r"(zb));
+  }
+}
+// The same for any zero point: q - z rounded to bf16 (both scalings are exact).
+__device__ __noinline__ uint32_t unpack_pair_any(uint32_t byte, float z) {
+  const float lo = __fsub_rn(static_cast<float>(byte & 0xFu), z) * 0.015625f;
+  const float hi = __fsub_rn(static_cast<float>(byte >> 4), z) * 0.015625f;
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     w4a16_experts_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC, Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * STAGES + 2 * CSTAGES + 5];
+  __shared__ __align__(8) uint64_t bars[2 * XSTAGES + 2 * ASTAGES + 2 * CSTAGES + 5];
   __shared__ uint32_t tmem_slot;
-  int* first_row = reinterpret_cast<int*>(smem + STAGES * STAGE_BYTES + CSTAGES * CSTAGE_BYTES);  // [E + 1]
-  int* first_tile = first_row + MAX_EXPERTS + 1;                                                   // [E + 1]
+  int* first_row = reinterpret_cast<int*>(smem + XSTAGES * X_BYTES + CSTAGES * CSTAGE_BYTES);  // [E + 1]
+  int* first_tile = first_row + MAX_EXPERTS + 1;                                               // [E + 1]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t bar0 = smem_u32(&bars[0]);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };                             // even CTA: operands ready
-  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };                 // MMAs done with stage
-  auto cfull_bar = [&](int c) { return bar0 + 8u * (2 * STAGES + c); };             // codes and parameters landed
-  auto cempty_bar = [&](int c) { return bar0 + 8u * (2 * STAGES + CSTAGES + c); };  // and read
-  auto accf_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 * CSTAGES + a); };      // tile accumulated
-  auto acce_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 * CSTAGES + 2 + a); };  // accumulator read
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * CSTAGES + 4);
+  auto xfull_bar = [&](int s) { return bar0 + 8u * s; };                      // even CTA: both halves of X' landed
+  auto xempty_bar = [&](int s) { return bar0 + 8u * (XSTAGES + s); };         // MMAs done with the token stage
+  auto afull_bar = [&](int s) { return bar0 + 8u * (2 * XSTAGES + s); };      // even CTA: both CTAs' rows unpacked
+  auto aempty_bar = [&](int s) { return bar0 + 8u * (2 * XSTAGES + ASTAGES + s); };
+  const uint32_t bar1 = bar0 + 8u * (2 * XSTAGES + 2 * ASTAGES);
+  auto cfull_bar = [&](int c) { return bar1 + 8u * c; };                      // codes and parameters landed
+  auto cempty_bar = [&](int c) { return bar1 + 8u * (CSTAGES + c); };         // and read
+  auto accf_bar = [&](int a) { return bar1 + 8u * (2 * CSTAGES + a); };       // group accumulated
+  auto acce_bar = [&](int a) { return bar1 + 8u * (2 * CSTAGES + 2 + a); };   // even CTA: accumulators read
+  const uint32_t drain_bar = bar1 + 8u * (2 * CSTAGES + 4);
   const uint32_t smem_base = smem_u32(smem);
-  auto a_tile = [&](int s) { return smem_base + static_cast<uint32_t>(s * STAGE_BYTES); };
-  auto x_tile = [&](int s) { return a_tile(s) + A_BYTES; };
-  auto c_tile = [&](int c) { return smem_base + static_cast<uint32_t>(STAGES * STAGE_BYTES + c * CSTAGE_BYTES); };
+  auto x_tile = [&](int s) { return smem_base + static_cast<uint32_t>(s * X_BYTES); };
+  auto c_tile = [&](int c) { return smem_base + static_cast<uint32_t>(XSTAGES * X_BYTES + c * CSTAGE_BYTES); };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1 + 2 * 4);    // TMA arm, and the stage's four dequantizer warps of both CTAs
-      mbar_init(empty_bar(s), 1);
+    for (int s = 0; s < XSTAGES; ++s) {
+      mbar_init(xfull_bar(s), 1);           // TMA arm
+      mbar_init(xempty_bar(s), 1);
+    }
+    for (int s = 0; s < ASTAGES; ++s) {
+      mbar_init(afull_bar(s), 2 * 4);       // the four unpacker warps of both CTAs
+      mbar_init(aempty_bar(s), 1);
     }
     for (int c = 0; c < CSTAGES; ++c) {
-      mbar_init(cfull_bar(c), 1 + 32);      // TMA arm, and the copies of each lane of warp 7
-      mbar_init(cempty_bar(c), DQ_WARPS);
+      mbar_init(cfull_bar(c), 1 + 32);      // TMA arm, and the copies of each lane of warp 3
+      mbar_init(cempty_bar(c), DQ_WARPS + EPI_WARPS);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf_bar(a), 1);
-      mbar_init(acce_bar(a), 8);            // 4 epilogue warps x 2 CTAs
+      mbar_init(acce_bar(a), 2 * EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     fence_barrier_init();
@@ -191,71 +257,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int n_pairs = static_cast<int>(gridDim.x >> 1);
   const int num_tiles = first_tile[p.E];
+  const int num_groups = p.num_kb / 2;
   const int num_slots = (p.num_kb + SLOT_KB - 1) / SLOT_KB;
   auto tile_at = [&](int t) { return tile_of(t, first_tile, first_row, p.E); };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------------------ TMA (token rows)
-    if (elect_one()) {
+  if (warp < FIRST_EPI) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    if (warp == 0 && elect_one()) {
+      // ------------------------------------------------------------------------------ TMA (token rows)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      const uint64_t pol = policy_evict_normal();
       for (int t = pair; ok && t < num_tiles; t += n_pairs) {
         const Tile tile = tile_at(t);
         const int half = static_cast<int>(tile.n() / 2);
         const int boxes = (half + X_BOX - 1) / X_BOX;
         const int32_t row = tile.row0 + static_cast<int32_t>(rank) * half;
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, st, p.limit_ns, kSiteTmaEmpty)) {
+          if (!mbar_wait(xempty_bar(stage), phase ^ 1u, st, p.limit_ns, kSiteTmaEmpty)) {
             ok = false;
             break;
           }
-          const uint32_t fb = map_to_rank(full_bar(stage), 0);
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(2 * boxes * X_BOX_BYTES));
-          const uint64_t pol = policy_evict_normal();
+          const uint32_t fb = map_to_rank(xfull_bar(stage), 0);
+          if (rank == 0) mbar_arrive_expect_tx(xfull_bar(stage), static_cast<uint32_t>(2 * boxes * X_BOX_BYTES));
           for (int b = 0; b < boxes; ++b)
             tma_load_2d_pair_hint(x_tile(stage) + static_cast<uint32_t>(b * X_BOX_BYTES), &tmX, kb * BK, row + b * X_BOX,
                                   fb, pol);
-          if (++stage == STAGES) {
+          if (++stage == XSTAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------------------ MMA (even CTA)
-    if (rank == 0 && elect_one()) {
-      int stage = 0, i = 0;
-      uint32_t phase = 0;
+    } else if (warp == 1 && rank == 0 && elect_one()) {
+      // ------------------------------------------------------------------------------ MMA (even CTA)
+      int xs = 0, as = 0;
+      uint32_t xphase = 0, aphase = 0;
+      uint32_t group = 0;  // groups issued so far: accumulator group & 1
       bool ok = true;
-      for (int t = pair; ok && t < num_tiles; t += n_pairs, ++i) {
+      for (int t = pair; ok && t < num_tiles; t += n_pairs) {
         const uint32_t idesc = idesc_bf16_f32(2 * HALF, tile_at(t).n());
-        const int acc = i & 1;
-        if (i >= 2 && !mbar_wait(acce_bar(acc), static_cast<uint32_t>(i / 2 - 1) & 1u, st, p.limit_ns, kSiteMmaAccEmpty)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!mbar_wait(full_bar(stage), phase, st, p.limit_ns, kSiteMmaFull)) {
+          const uint32_t acc = group & 1u;
+          if ((kb & 1) == 0 && group >= 2 &&
+              !mbar_wait(acce_bar(acc), (group / 2 - 1) & 1u, st, p.limit_ns, kSiteMmaAccEmpty)) {
+            ok = false;
+            break;
+          }
+          if (!mbar_wait(xfull_bar(xs), xphase, st, p.limit_ns, kSiteMmaFull) ||
+              !mbar_wait(afull_bar(as), aphase, st, p.limit_ns, kSiteMmaFull)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          const uint32_t a = tmem_base + A_COL0 + static_cast<uint32_t>(as * A_COLS);
 #pragma unroll
           for (int kk = 0; kk < BK / UK; ++kk)
-            umma_bf16_pair(tmem_base + static_cast<uint32_t>(acc * BN), smem_desc_sw128(a_tile(stage) + kk * UK * 2),
-                           smem_desc_sw128(x_tile(stage) + kk * UK * 2), idesc, (kb | kk) != 0 ? 1u : 0u);
-          umma_commit_pair(empty_bar(stage), 0x3);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            umma_bf16_pair_ts(tmem_base + acc * BN, a + static_cast<uint32_t>(kk * UK / 2),
+                              smem_desc_sw128(x_tile(xs) + kk * UK * 2), idesc, ((kb & 1) | kk) != 0 ? 1u : 0u);
+          umma_commit_pair(aempty_bar(as), 0x3);
+          umma_commit_pair(xempty_bar(xs), 0x3);
+          if (kb & 1) {
+            umma_commit_pair(accf_bar(acc), 0x3);
+            ++group;
+          }
+          if (++xs == XSTAGES) {
+            xs = 0;
+            xphase ^= 1u;
+          }
+          if (++as == ASTAGES) {
+            as = 0;
+            aphase ^= 1u;
           }
         }
-        if (!ok) break;
-        umma_commit_pair(accf_bar(acc), 0x3);
       }
       umma_commit_pair(drain_bar, 0x1);
       const uint64_t t0 = global_timer_ns();
@@ -264,11 +339,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           raise_timeout(st, kSiteDrainMma);
           break;
         }
-    }
-    __syncwarp();
-  } else if (warp == 6) {
-    // ------------------------------------------------------------------------------ TMA (codes)
-    if (elect_one()) {
+    } else if (warp == 2 && elect_one()) {
+      // ------------------------------------------------------------------------------ TMA (codes)
       bool ok = true;
       int slot = 0;
       uint32_t phase = 0;
@@ -298,118 +370,184 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         }
       }
-    }
-    __syncwarp();
-  } else if (warp == 7) {
-    // ------------------------------------------------------------------------------ steps and zero points
-    bool ok = true;
-    int slot = 0;
-    uint32_t phase = 0;
-    const int num_groups = p.num_kb / 2;
-    for (int t = pair; ok && t < num_tiles; t += n_pairs) {
-      const Tile tile = tile_at(t);
-      int64_t row[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = lane + 32 * i;
-        int64_t o;  // rows past the end read the last row: what comes of them is not stored
-        if (GATED)
-          o = min(static_cast<int64_t>(tile.band) * HALF + rank * (HALF / 2) + i * 16 + (r & 15), p.O / 2 - 1) +
-              ((r >> 4) & 1) * (p.O / 2);
-        else
-          o = min(static_cast<int64_t>(tile.band) * 2 * HALF + rank * HALF + r, p.O - 1);
-        row[i] = (static_cast<int64_t>(tile.e) * p.O + o) * p.G;
-      }
-      for (int j = 0; j < num_slots; ++j) {
-        if (!dq::warp_wait_any(cempty_bar(slot), phase ^ 1u, st, p.limit_ns, kSiteTmaProduced, false)) {
-          ok = false;
-          break;
-        }
-        const int g = 2 * j;
-        const uint32_t dst = c_tile(slot) + C_BYTES + static_cast<uint32_t>(lane * 8);
+    } else if (warp == 3) {
+      // ------------------------------------------------------------------------------ steps and zero points
+      bool ok = true;
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int t = pair; ok && t < num_tiles; t += n_pairs) {
+        const Tile tile = tile_at(t);
+        int64_t row[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t d = dst + static_cast<uint32_t>(i * 256);
-          if (p.pair_params) {
-            few::cp_async8(d, p.steps + row[i] + g);
-            few::cp_async8(d + P_BYTES, p.zeros + row[i] + g);
-          } else {
-            few::cp_async4(d, p.steps + row[i] + g);
-            few::cp_async4(d + P_BYTES, p.zeros + row[i] + g);
-            if (g + 1 < num_groups) {
-              few::cp_async4(d + 4, p.steps + row[i] + g + 1);
-              few::cp_async4(d + P_BYTES + 4, p.zeros + row[i] + g + 1);
+          const int r = lane + 32 * i;
+          int64_t o;  // rows past the end read the last row: what comes of them is not stored
+          if (GATED)
+            o = min(static_cast<int64_t>(tile.band) * HALF + rank * (HALF / 2) + i * 16 + (r & 15), p.O / 2 - 1) +
+                ((r >> 4) & 1) * (p.O / 2);
+          else
+            o = min(static_cast<int64_t>(tile.band) * 2 * HALF + rank * HALF + r, p.O - 1);
+          row[i] = (static_cast<int64_t>(tile.e) * p.O + o) * p.G;
+        }
+        for (int j = 0; j < num_slots; ++j) {
+          if (!dq::warp_wait_any(cempty_bar(slot), phase ^ 1u, st, p.limit_ns, kSiteTmaProduced, false)) {
+            ok = false;
+            break;
+          }
+          const int g = 2 * j;
+          const uint32_t dst = c_tile(slot) + C_BYTES + static_cast<uint32_t>(lane * 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t d = dst + static_cast<uint32_t>(i * 256);
+            if (p.pair_params) {
+              few::cp_async8(d, p.steps + row[i] + g);
+              few::cp_async8(d + P_BYTES, p.zeros + row[i] + g);
+            } else {
+              few::cp_async4(d, p.steps + row[i] + g);
+              few::cp_async4(d + P_BYTES, p.zeros + row[i] + g);
+              if (g + 1 < num_groups) {
+                few::cp_async4(d + 4, p.steps + row[i] + g + 1);
+                few::cp_async4(d + P_BYTES + 4, p.zeros + row[i] + g + 1);
+              }
             }
           }
-        }
-        cp_async_arrive(cfull_bar(slot));
-        if (++slot == CSTAGES) {
-          slot = 0;
-          phase ^= 1u;
+          cp_async_arrive(cfull_bar(slot));
+          if (++slot == CSTAGES) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
       }
+      few::cp_async_wait_all();
     }
-    few::cp_async_wait_all();
+    __syncwarp();
   } else if (warp >= FIRST_DQ) {
-    // ------------------------------------------------------------------------------ dequantizers
-    const int s_own = (warp - FIRST_DQ) / 4;
-    const int r = lane + 32 * ((warp - FIRST_DQ) & 3);  // the lane's row of the CTA's 128
+    // ------------------------------------------------------------------------------ unpackers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    const int set = (warp - FIRST_DQ) / 4;
+    const int quarter = warp & 3;
+    const int r = lane + 32 * quarter;  // the lane's row of the CTA's 128
+    const uint32_t sw = static_cast<uint32_t>(r & 7);
     bool ok = true;
-    int slot = 0, use = 0, first = s_own;  // first: this set's k-block of the tile's first slot
-    uint32_t phase = 0;
+    int slot = 0;
+    uint32_t phase = 0, use = 0;  // k-blocks that this set has filled: buffer set + 2 (use & 1)
     for (int t = pair; ok && t < num_tiles; t += n_pairs) {
-      for (int j = 0; j < num_slots; ++j) {
+      for (int j = 0; ok && j < num_slots; ++j) {
         if (!dq::warp_wait_any(cfull_bar(slot), phase, st, p.limit_ns, kSiteTmaEmpty, false)) {
           ok = false;
           break;
         }
-        const bool mine = j * SLOT_KB + first < p.num_kb;
-        uint32_t v[32];
-        if (mine) {
-          const uint32_t line = c_tile(slot) + static_cast<uint32_t>(r * 128);
-          const uint32_t sw = static_cast<uint32_t>(r & 7);
-          const uint4 w0 = few::lds128(line + (((2u * first) ^ sw) << 4));
-          const uint4 w1 = few::lds128(line + (((2u * first + 1u) ^ sw) << 4));
-          const uint32_t pa = c_tile(slot) + C_BYTES + static_cast<uint32_t>(r * 8 + (first >> 1) * 4);
-          float stp, z;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(stp) : "r"(pa) : "memory");
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(pa + P_BYTES) : "memory");
+        const uint32_t line = c_tile(slot) + static_cast<uint32_t>(r * 128);
+        const uint32_t pa = c_tile(slot) + C_BYTES + P_BYTES + static_cast<uint32_t>(r * 8);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // this set's k-blocks of the slot: set and set + 2, groups 2 j and 2 j + 1
+          const int kb = set + 2 * i;
+          const bool mine = j * SLOT_KB + kb < p.num_kb;  // the last slot may hold one group
+          uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
+          float z = 0.0f;
+          if (mine) {
+            w0 = few::lds128(line + (((2u * kb) ^ sw) << 4));
+            w1 = few::lds128(line + (((2u * kb + 1u) ^ sw) << 4));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(pa + 4u * i) : "memory");
+          }
+          if (i == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cempty_bar(slot));
+          }
+          if (!mine) break;
+          const uint32_t buf = static_cast<uint32_t>(set) + 2u * (use & 1u);
+          if (use >= 2 && !dq::warp_wait_any(aempty_bar(static_cast<int>(buf)), ((use >> 1) - 1u) & 1u, st, p.limit_ns,
+                                             kSiteMmaFull, true)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();  // the MMAs that read the buffer come before the stores below
+          ++use;
+          const uint32_t ta = tmem_base + A_COL0 + buf * A_COLS + (static_cast<uint32_t>(quarter * 32) << 16);
           const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-          dequant_words<8>(w, z, stp, v);
+          uint32_t o[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (fabsf(z) <= 240.0f) {
+              const __nv_bfloat162 zz = __float2bfloat162_rn(z * -0.015625f);
+              const uint32_t zb = *reinterpret_cast<const uint32_t*>(&zz);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) unpack_word(w[4 * h + c], zb, o + 4 * c);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) o[c] = unpack_pair_any((w[4 * h + c / 4] >> (8 * (c & 3))) & 0xFFu, z);
+            }
+            __syncwarp();
+            tmem_st16(ta + static_cast<uint32_t>(16 * h), o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(map_to_rank(afull_bar(static_cast<int>(buf)), 0));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(cempty_bar(slot));
         if (++slot == CSTAGES) {
           slot = 0;
           phase ^= 1u;
         }
-        if (!mine) continue;
-        if (use > 0 && !dq::warp_wait_any(empty_bar(s_own), static_cast<uint32_t>(use - 1) & 1u, st, p.limit_ns,
-                                          kSiteMmaFull, true)) {
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------------------ scaling and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
+    const int quarter = warp & 3, half = (warp - FIRST_EPI) / 4;
+    const int r = lane + 32 * quarter;
+    int slot = 0;
+    uint32_t phase = 0, group = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < num_tiles; t += n_pairs) {
+      const Tile tile = tile_at(t);
+      const int chunks = static_cast<int>(tile.n() / 16);
+      const int mine = (chunks - half + 1) / 2;  // this warp's blocks: half, half + 2, ...
+      uint64_t y[CHUNKS][8];
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[c][k] = 0ull;
+      float2 steps = make_float2(0.0f, 0.0f);
+      for (int g = 0; g < num_groups; ++g, ++group) {
+        if ((g & 1) == 0) {
+          if (!dq::warp_wait_any(cfull_bar(slot), phase, st, p.limit_ns, kSiteTmaEmpty, false)) {
+            ok = false;
+            break;
+          }
+          steps = few::lds64f(c_tile(slot) + C_BYTES + static_cast<uint32_t>(r * 8));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(cempty_bar(slot));
+          if (++slot == CSTAGES) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+        const uint32_t s64 = __float_as_uint(((g & 1) ? steps.y : steps.x) * 64.0f);
+        const uint64_t ss = f32x2_pack(s64, s64);
+        const uint32_t acc = group & 1u;
+        if (!dq::warp_wait_any(accf_bar(static_cast<int>(acc)), (group >> 1) & 1u, st, p.limit_ns, kSiteEpiAccFull, false)) {
           ok = false;
           break;
         }
-        ++use;
-        store_words_sw128<8>(v, a_tile(s_own) + static_cast<uint32_t>(r) * 128u, r, 0);
-        fence_proxy_async_smem();  // the tensor cores read these bytes through the async proxy
+        tc_fence_after();
+        const uint32_t ta = tmem_base + acc * BN + static_cast<uint32_t>(half * 16) + (static_cast<uint32_t>(quarter * 32) << 16);
+        uint32_t v[2][16];
+        if (mine > 0) dq::tmem_ld16_issue(ta, v[0]);
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+          if (c >= mine) break;
+          dq::tmem_wait_ld16(v[c & 1]);
+          if (c + 1 < mine) dq::tmem_ld16_issue(ta + static_cast<uint32_t>((c + 1) * 32), v[(c + 1) & 1]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) fma_f32x2(y[c][k], ss, v[c & 1][2 * k], v[c & 1][2 * k + 1]);
+        }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_to_rank(full_bar(s_own), 0));
+        if (lane == 0) mbar_arrive_remote(map_to_rank(acce_bar(static_cast<int>(acc)), 0));
       }
-      // k-blocks are numbered through the pair's tiles: stage = number % STAGES, so a tile whose k-blocks are
-      // no multiple of STAGES moves the sets
-      first = (first + SLOT_KB - p.num_kb % SLOT_KB) % SLOT_KB;
-    }
-  } else {
-    // ------------------------------------------------------------------------------ epilogue
-    const int quarter = warp & 3;
-    int i = 0;
-    for (int t = pair; t < num_tiles; t += n_pairs, ++i) {
-      const Tile tile = tile_at(t);
-      const int acc = i & 1;
-      if (!dq::warp_wait_any(accf_bar(acc), static_cast<uint32_t>(i / 2) & 1u, st, p.limit_ns, kSiteEpiAccFull, false)) break;
-      tc_fence_after();
-      const uint32_t ta = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int chunks = static_cast<int>(tile.n() / 16);
+      if (!ok) break;
+
       int64_t o, n_out;
       if (GATED) {
         n_out = p.O / 2;
@@ -419,44 +557,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         o = static_cast<int64_t>(tile.band) * 2 * HALF + rank * HALF + quarter * 32 + lane;
       }
       const bool real = o < n_out;
-      uint16_t* y = p.Y + static_cast<int64_t>(tile.row0) * p.ldy + o;
-      auto emit = [&](const uint32_t (&v)[16], int c) {
-        if (GATED) {
-          // lanes 0-15 hold the gate of both tokens of a pair, lanes 16-31 the up value: each half gets what it
-          // lacks for one of the two tokens
-          const bool low = lane < 16;
+      uint16_t* dst = p.Y + static_cast<int64_t>(tile.row0) * p.ldy + o;
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, low ? v[k + 1] : v[k], 16));
-            const float own = __uint_as_float(low ? v[k] : v[k + 1]);
+      for (int c = 0; c < CHUNKS; ++c) {
+        if (c >= mine) break;
+        const int tok0 = (2 * c + half) * 16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t lo, hi;
+          asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(y[c][k]));
+          if (GATED) {
+            // lanes 0-15 hold the gate of both tokens of a pair, lanes 16-31 the up value: each half gets what it
+            // lacks for one of the two tokens
+            const bool low = lane < 16;
+            const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, low ? hi : lo, 16));
+            const float own = __uint_as_float(low ? lo : hi);
             const float out = few::silu(low ? own : other) * (low ? other : own);
-            const int tok = c * 16 + k + (low ? 0 : 1);
+            const int tok = tok0 + 2 * k + (low ? 0 : 1);
             const __nv_bfloat16 b = __float2bfloat16_rn(out);
-            if (real && tok < tile.tokens) y[tok * p.ldy] = *reinterpret_cast<const uint16_t*>(&b);
+            if (real && tok < tile.tokens) dst[tok * p.ldy] = *reinterpret_cast<const uint16_t*>(&b);
+          } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&b);
+            const int tok = tok0 + 2 * k;
+            if (real && tok < tile.tokens) dst[tok * p.ldy] = static_cast<uint16_t>(u);
+            if (real && tok + 1 < tile.tokens) dst[(tok + 1) * p.ldy] = static_cast<uint16_t>(u >> 16);
           }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(v[k]));
-            if (real && c * 16 + k < tile.tokens) y[(c * 16 + k) * p.ldy] = *reinterpret_cast<const uint16_t*>(&b);
-          }
-        }
-      };
-      uint32_t va[16], vb[16];
-      dq::tmem_ld16_issue(ta, va);
-      for (int c = 0; c < chunks; c += 2) {
-        dq::tmem_wait_ld16(va);
-        if (c + 1 < chunks) dq::tmem_ld16_issue(ta + static_cast<uint32_t>((c + 1) * 16), vb);
-        emit(va, c);
-        if (c + 1 < chunks) {
-          dq::tmem_wait_ld16(vb);
-          if (c + 2 < chunks) dq::tmem_ld16_issue(ta + static_cast<uint32_t>((c + 2) * 16), va);
-          emit(vb, c + 1);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(map_to_rank(acce_bar(acc), 0));
     }
     __syncwarp();
   }
