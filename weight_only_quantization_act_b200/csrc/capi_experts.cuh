@@ -288,8 +288,8 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   const int64_t n_bands = ((gated ? O / 2 : O) + tile_out - 1) / tile_out;
   if (E * O >= (1ll << 31) || (R / awq::grp::BN + E) * n_bands >= (1ll << 31))
     return fail(AWQ_ERR_INVALID_ARG, "too many weight rows or tiles");
-  CUtensorMap tmX, tmC;
-  AWQ_TRY(make_tmap(&tmX, Xs, R, K, ldx, awq::grp::X_BOX));
+  CUtensorMap tmX[3], tmC;  // boxes of 32, 64 and 96 rows
+  for (int i = 0; i < 3; ++i) AWQ_TRY(make_tmap(&tmX[i], Xs, R, K, ldx, (i + 1) * awq::grp::X_BOX));
   AWQ_TRY(make_tmap_codes_sw128(&tmC, codes, E * O, K / 8, gated ? 16 : awq::grp::HALF));
   awq::grp::Params q = {};
   q.offsets = offsets;
@@ -303,15 +303,16 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   q.E = static_cast<int>(E);
   q.min_rows = kFewRows + 1;
   q.n_bands = static_cast<int>(n_bands);
-  q.num_kb = static_cast<int>(K / awq::grp::BK);
   q.pair_params = p.pair_params;
   q.status = static_cast<awq::DeviceStatus*>(workspace);
   q.limit_ns = g_wait_limit_ns.load();
   const unsigned ctas = static_cast<unsigned>(2 * d->expert_clusters);
   if (gated)
-    awq::grp::w4a16_experts_kernel<true><<<ctas, awq::grp::THREADS, awq::grp::SMEM_BYTES, st>>>(tmX, tmC, q);
+    awq::grp::w4a16_experts_kernel<true><<<ctas, awq::grp::THREADS, awq::grp::SMEM_BYTES, st>>>(tmX[0], tmX[1], tmX[2],
+                                                                                                  tmC, q);
   else
-    awq::grp::w4a16_experts_kernel<false><<<ctas, awq::grp::THREADS, awq::grp::SMEM_BYTES, st>>>(tmX, tmC, q);
+    awq::grp::w4a16_experts_kernel<false><<<ctas, awq::grp::THREADS, awq::grp::SMEM_BYTES, st>>>(tmX[0], tmX[1], tmX[2],
+                                                                                                  tmC, q);
   AWQ_TRY(check_launch("w4a16_experts_kernel"));
   return ok();
 }

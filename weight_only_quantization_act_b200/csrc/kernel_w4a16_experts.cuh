@@ -24,16 +24,19 @@
 //
 // Persistent, clusters of 2 CTAs, one CTA per SM; every CTA makes the table of tiles from the row offsets for
 // itself and takes each n-th tile, so nothing is exchanged between pairs. Warps of a CTA:
-//   0      TMA of this CTA's half of the tile's token rows (boxes of 32 rows x 64 in-features, 128-byte swizzle)
-//          into a ring of 8, counted on the even CTA's barrier
+//   0      TMA of this CTA's half of the tile's token rows, a group at a time (two boxes of 64 in-features, 128-byte
+//          swizzle, the box's height 32, 64 or 96 rows), into a ring of 4
 //   1      tensor memory; the even CTA issues the pair MMAs (cta_group::2, M = 256, N, K = 16, A from tensor memory)
 //          into two accumulators in turn, one group each
 //   2      TMA of the code words, 128 rows x 256 in-features at a time (128 bytes of a row), into a ring of its own
 //   3      steps and zero points of those rows and groups by cp.async, counted on the same barrier
 //   4-11   scaling and epilogue: two warps per quarter of the rows, alternate blocks of 16 tokens
-//   12-19  unpackers: two sets of four warps on alternate k-blocks of 64 in-features, a weight row per lane, into
-//          four operand buffers
-// Every wait is bounded.
+//   12-19  unpackers: two sets of four warps, one for each half of a group, a weight row per lane, into two operand
+//          buffers
+// The thread that issues the MMAs waits once per group: one barrier counts the token rows, the unpacked operand and the
+// reading of the accumulator that the group will overwrite, and one commit per group tells all three that it is done
+// (with a wait and a commit for each, and per 64 in-features, that thread took 1700 cycles per group). Every wait
+// is bounded.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -51,14 +54,12 @@ constexpr int HALF = 128;                         // weight rows per CTA
 constexpr int BN = 192;                           // tokens per tile at most
 constexpr int BK = 64;
 constexpr int UK = 16;
-constexpr int XSTAGES = 8;                        // token ring
-constexpr int X_BOX = 32;                         // token rows per TMA box
-constexpr int X_BOX_BYTES = X_BOX * BK * 2;
-constexpr int X_BYTES = BN / 2 * BK * 2;          // 12 KB  this CTA's token rows
-constexpr int ASTAGES = 4;                        // operand buffers in tensor memory
-constexpr int A_COLS = BK / 2;                    // two in-features per 32-bit column
-constexpr int CSTAGES = 4;                        // code ring
-constexpr int SLOT_KB = 4;                        // k-blocks per code slot: 32 words = 128 bytes of each row
+constexpr int STAGES = 4;                         // token ring, and ring of group barriers
+constexpr int X_BOX = 32;                         // token rows per TMA box: this, twice or three times it
+constexpr int X_HALF_BYTES = BN / 2 * BK * 2;     // 12 KB  this CTA's token rows, 64 in-features
+constexpr int X_BYTES = 2 * X_HALF_BYTES;
+constexpr int A_COLS = BK;                        // operand buffer: two in-features per 32-bit column, 128 of them
+constexpr int CSTAGES = 4;                        // code ring: two groups per slot, 32 words = 128 bytes of each row
 constexpr int C_BYTES = HALF * 128;               // 16 KB  code words
 constexpr int P_BYTES = HALF * 2 * 4;             // 1 KB   steps (zero points) of two groups
 constexpr int CSTAGE_BYTES = C_BYTES + 2 * P_BYTES;
@@ -72,13 +73,13 @@ static_assert(32 * (EPI_WARPS * EPI_REGS + (THREADS / 32 - EPI_WARPS) * OTHER_RE
 constexpr int CHUNKS = BN / 16 / 2;               // blocks of 16 tokens per scaling warp
 constexpr int MAX_EXPERTS = 1024;
 constexpr int TABLE_BYTES = 2 * (MAX_EXPERTS + 1) * 4;
-constexpr int SMEM_BYTES = XSTAGES * X_BYTES + CSTAGES * CSTAGE_BYTES + TABLE_BYTES + 1024;
+constexpr int SMEM_BYTES = STAGES * X_BYTES + CSTAGES * CSTAGE_BYTES + TABLE_BYTES + 1024;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t A_COL0 = 2 * BN;
-static_assert(A_COL0 + ASTAGES * A_COLS <= TMEM_COLS, "accumulators and operand buffers fit tensor memory");
+static_assert(A_COL0 + 2 * A_COLS <= TMEM_COLS, "accumulators and operand buffers fit tensor memory");
 static_assert(SMEM_BYTES <= 232448, "fits the 227 KB of dynamic shared memory");
-static_assert(X_BYTES % 1024 == 0 && CSTAGE_BYTES % 1024 == 0 && X_BYTES % X_BOX_BYTES == 0,
-              "tiles stay 1024-byte aligned and whole boxes fit");
+static_assert(X_HALF_BYTES % 1024 == 0 && CSTAGE_BYTES % 1024 == 0 && BN / 2 == 3 * X_BOX,
+              "tiles stay 1024-byte aligned and the largest box fits");
 
 struct Params {
   const int* offsets;      // [E + 1]
@@ -89,7 +90,6 @@ struct Params {
   int E;
   int min_rows;            // experts with fewer rows are left to another kernel
   int n_bands;             // tiles along the weight rows
-  int num_kb;              // K / 64
   int pair_params;         // steps and zero points of two groups can be copied as 8 bytes
   DeviceStatus* status;
   uint64_t limit_ns;
@@ -139,6 +139,12 @@ __device__ __forceinline__ void umma_bf16_pair_ts(uint32_t d_tmem, uint32_t a_tm
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Arrive on a barrier of either CTA of the pair after tensor-memory accesses alone, which the tcgen05 fences around
+// it order: no release of this thread's other writes to the cluster (a fence that takes longer than the unpacking of a
+// k-block).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -167,57 +173,67 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t zb, uint32_t* o
   }
 }
 // The same for any zero point: q - z rounded to bf16 (both scalings are exact).
-__device__ __noinline__ uint32_t unpack_pair_any(uint32_t byte, float z) {
+__device__ __forceinline__ uint32_t unpack_pair_any(uint32_t byte, float z) {
   const float lo = __fsub_rn(static_cast<float>(byte & 0xFu), z) * 0.015625f;
   const float hi = __fsub_rn(static_cast<float>(byte >> 4), z) * 0.015625f;
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Bounded wait: the hardware suspends the waiting threads for up to 20 us per try. One that gives up, after the limit or
+// because another has, returns like any other: the roles run on to the end of their tile, where they look at the
+// status, so that a wait costs its poll and one branch in the loops (a result to carry and test cost the scaling warps a
+// third of their instructions).
+constexpr uint32_t SLEEP_NS = 20000;
+__device__ __forceinline__ void wait_slow(uint32_t bar, uint32_t parity, DeviceStatus* st, uint64_t limit, unsigned where) {
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait_sleep(bar, parity, SLEEP_NS)) {
+    if (status_code(st) != 0u) return;
+    if (global_timer_ns() - t0 > limit) {
+      raise_timeout(st, where);
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, const Params& p, unsigned where) {
+  if (!mbar_try_wait_sleep(bar, parity, SLEEP_NS)) wait_slow(bar, parity, p.status, p.limit_ns, where);
+}
+
 template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    w4a16_experts_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC, Params p) {
+    w4a16_experts_kernel(const __grid_constant__ CUtensorMap tmX1, const __grid_constant__ CUtensorMap tmX2,
+                         const __grid_constant__ CUtensorMap tmX3, const __grid_constant__ CUtensorMap tmC, Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * XSTAGES + 2 * ASTAGES + 2 * CSTAGES + 5];
+  __shared__ __align__(8) uint64_t bars[2 * STAGES + 2 * CSTAGES + 1];
   __shared__ uint32_t tmem_slot;
-  int* first_row = reinterpret_cast<int*>(smem + XSTAGES * X_BYTES + CSTAGES * CSTAGE_BYTES);  // [E + 1]
-  int* first_tile = first_row + MAX_EXPERTS + 1;                                               // [E + 1]
+  int* first_row = reinterpret_cast<int*>(smem + STAGES * X_BYTES + CSTAGES * CSTAGE_BYTES);  // [E + 1]
+  int* first_tile = first_row + MAX_EXPERTS + 1;                                              // [E + 1]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t bar0 = smem_u32(&bars[0]);
-  auto xfull_bar = [&](int s) { return bar0 + 8u * s; };                      // even CTA: both halves of X' landed
-  auto xempty_bar = [&](int s) { return bar0 + 8u * (XSTAGES + s); };         // MMAs done with the token stage
-  auto afull_bar = [&](int s) { return bar0 + 8u * (2 * XSTAGES + s); };      // even CTA: both CTAs' rows unpacked
-  auto aempty_bar = [&](int s) { return bar0 + 8u * (2 * XSTAGES + ASTAGES + s); };
-  const uint32_t bar1 = bar0 + 8u * (2 * XSTAGES + 2 * ASTAGES);
-  auto cfull_bar = [&](int c) { return bar1 + 8u * c; };                      // codes and parameters landed
-  auto cempty_bar = [&](int c) { return bar1 + 8u * (CSTAGES + c); };         // and read
-  auto accf_bar = [&](int a) { return bar1 + 8u * (2 * CSTAGES + a); };       // group accumulated
-  auto acce_bar = [&](int a) { return bar1 + 8u * (2 * CSTAGES + 2 + a); };   // even CTA: accumulators read
-  const uint32_t drain_bar = bar1 + 8u * (2 * CSTAGES + 4);
+  // group i of this pair's tiles, numbered through them: stage i % 4, phase i / 4; accumulator and operand i % 2
+  auto full_bar = [&](uint32_t i) { return bar0 + 8u * (i % STAGES); };             // even CTA: group can be issued
+  auto done_bar = [&](uint32_t i) { return bar0 + 8u * (STAGES + i % STAGES); };    // group accumulated
+  auto parity = [](uint32_t i) { return (i / STAGES) & 1u; };
+  auto cfull_bar = [&](int c) { return bar0 + 8u * (2 * STAGES + c); };             // codes and parameters landed
+  auto cempty_bar = [&](int c) { return bar0 + 8u * (2 * STAGES + CSTAGES + c); };  // and read
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * CSTAGES);
   const uint32_t smem_base = smem_u32(smem);
-  auto x_tile = [&](int s) { return smem_base + static_cast<uint32_t>(s * X_BYTES); };
-  auto c_tile = [&](int c) { return smem_base + static_cast<uint32_t>(XSTAGES * X_BYTES + c * CSTAGE_BYTES); };
+  auto x_tile = [&](uint32_t i) { return smem_base + (i % STAGES) * X_BYTES; };
+  auto c_tile = [&](int c) { return smem_base + static_cast<uint32_t>(STAGES * X_BYTES + c * CSTAGE_BYTES); };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < XSTAGES; ++s) {
-      mbar_init(xfull_bar(s), 1);           // TMA arm
-      mbar_init(xempty_bar(s), 1);
-    }
-    for (int s = 0; s < ASTAGES; ++s) {
-      mbar_init(afull_bar(s), 2 * 4);       // the four unpacker warps of both CTAs
-      mbar_init(aempty_bar(s), 1);
+    for (uint32_t s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1 + 2 * DQ_WARPS + 2 * EPI_WARPS);  // TMA arm; both CTAs' unpackers and scaling warps
+      mbar_init(done_bar(s), 1);
     }
     for (int c = 0; c < CSTAGES; ++c) {
       mbar_init(cfull_bar(c), 1 + 32);      // TMA arm, and the copies of each lane of warp 3
       mbar_init(cempty_bar(c), DQ_WARPS + EPI_WARPS);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(accf_bar(a), 1);
-      mbar_init(acce_bar(a), 2 * EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     fence_barrier_init();
@@ -225,7 +241,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), TMEM_COLS);
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmX1);
+    tma_prefetch_desc(&tmX2);
+    tma_prefetch_desc(&tmX3);
     tma_prefetch_desc(&tmC);
   }
   // the table of tiles, with the rows clamped so that whatever stands in offsets no access leaves X and Y
@@ -257,79 +275,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int n_pairs = static_cast<int>(gridDim.x >> 1);
   const int num_tiles = first_tile[p.E];
-  const int num_groups = p.num_kb / 2;
-  const int num_slots = (p.num_kb + SLOT_KB - 1) / SLOT_KB;
+  const int num_groups = static_cast<int>(p.G);
+  const int num_slots = (num_groups + 1) / 2;
   auto tile_at = [&](int t) { return tile_of(t, first_tile, first_row, p.E); };
 
   if (warp < FIRST_EPI) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
     if (warp == 0 && elect_one()) {
       // ------------------------------------------------------------------------------ TMA (token rows)
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
+      uint32_t i = 0;
       const uint64_t pol = policy_evict_normal();
-      for (int t = pair; ok && t < num_tiles; t += n_pairs) {
+      for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
         const Tile tile = tile_at(t);
         const int half = static_cast<int>(tile.n() / 2);
         const int boxes = (half + X_BOX - 1) / X_BOX;
+        const CUtensorMap* map = boxes == 1 ? &tmX1 : boxes == 2 ? &tmX2 : &tmX3;
+        const uint32_t bytes = static_cast<uint32_t>(boxes * X_BOX * BK * 2 * 2 * 2);  // both halves, both CTAs
         const int32_t row = tile.row0 + static_cast<int32_t>(rank) * half;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!mbar_wait(xempty_bar(stage), phase ^ 1u, st, p.limit_ns, kSiteTmaEmpty)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = map_to_rank(xfull_bar(stage), 0);
-          if (rank == 0) mbar_arrive_expect_tx(xfull_bar(stage), static_cast<uint32_t>(2 * boxes * X_BOX_BYTES));
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d_pair_hint(x_tile(stage) + static_cast<uint32_t>(b * X_BOX_BYTES), &tmX, kb * BK, row + b * X_BOX,
-                                  fb, pol);
-          if (++stage == XSTAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        for (int g = 0; g < num_groups; ++g, ++i) {
+          if (i >= STAGES) wait(done_bar(i), parity(i - STAGES), p, kSiteTmaEmpty);
+          const uint32_t fb = map_to_rank(full_bar(i), 0);
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(i), bytes);
+          tma_load_2d_pair_hint(x_tile(i), map, g * 2 * BK, row, fb, pol);
+          tma_load_2d_pair_hint(x_tile(i) + X_HALF_BYTES, map, g * 2 * BK + BK, row, fb, pol);
         }
       }
     } else if (warp == 1 && rank == 0 && elect_one()) {
       // ------------------------------------------------------------------------------ MMA (even CTA)
-      int xs = 0, as = 0;
-      uint32_t xphase = 0, aphase = 0;
-      uint32_t group = 0;  // groups issued so far: accumulator group & 1
-      bool ok = true;
-      for (int t = pair; ok && t < num_tiles; t += n_pairs) {
+      uint32_t i = 0;
+      const uint64_t desc0 = smem_desc_sw128(x_tile(0));
+      for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
         const uint32_t idesc = idesc_bf16_f32(2 * HALF, tile_at(t).n());
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          const uint32_t acc = group & 1u;
-          if ((kb & 1) == 0 && group >= 2 &&
-              !mbar_wait(acce_bar(acc), (group / 2 - 1) & 1u, st, p.limit_ns, kSiteMmaAccEmpty)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait(xfull_bar(xs), xphase, st, p.limit_ns, kSiteMmaFull) ||
-              !mbar_wait(afull_bar(as), aphase, st, p.limit_ns, kSiteMmaFull)) {
-            ok = false;
-            break;
-          }
+        for (int g = 0; g < num_groups; ++g, ++i) {
+          wait(full_bar(i), parity(i), p, kSiteMmaFull);
           tc_fence_after();
-          const uint32_t a = tmem_base + A_COL0 + static_cast<uint32_t>(as * A_COLS);
+          const uint32_t d = tmem_base + (i & 1u) * BN;
+          const uint32_t a = tmem_base + A_COL0 + (i & 1u) * A_COLS;
+          const uint64_t b = desc0 + (i % STAGES) * (X_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / UK; ++kk)
-            umma_bf16_pair_ts(tmem_base + acc * BN, a + static_cast<uint32_t>(kk * UK / 2),
-                              smem_desc_sw128(x_tile(xs) + kk * UK * 2), idesc, ((kb & 1) | kk) != 0 ? 1u : 0u);
-          umma_commit_pair(aempty_bar(as), 0x3);
-          umma_commit_pair(xempty_bar(xs), 0x3);
-          if (kb & 1) {
-            umma_commit_pair(accf_bar(acc), 0x3);
-            ++group;
-          }
-          if (++xs == XSTAGES) {
-            xs = 0;
-            xphase ^= 1u;
-          }
-          if (++as == ASTAGES) {
-            as = 0;
-            aphase ^= 1u;
-          }
+          for (int kk = 0; kk < 2 * BK / UK; ++kk)  // 16 in-features: 8 columns of A, 32 bytes of B's rows
+            umma_bf16_pair_ts(d, a + static_cast<uint32_t>(kk * UK / 2),
+                              b + static_cast<uint64_t>(((kk >> 2) * X_HALF_BYTES + (kk & 3) * UK * 2) >> 4), idesc,
+                              kk != 0 ? 1u : 0u);
+          umma_commit_pair(done_bar(i), 0x3);
         }
       }
       umma_commit_pair(drain_bar, 0x1);
@@ -341,17 +329,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 2 && elect_one()) {
       // ------------------------------------------------------------------------------ TMA (codes)
-      bool ok = true;
       int slot = 0;
       uint32_t phase = 0;
-      for (int t = pair; ok && t < num_tiles; t += n_pairs) {
+      for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
         const Tile tile = tile_at(t);
         const int32_t w0 = tile.e * static_cast<int32_t>(p.O);
         for (int j = 0; j < num_slots; ++j) {
-          if (!mbar_wait(cempty_bar(slot), phase ^ 1u, st, p.limit_ns, kSiteTmaProduced)) {
-            ok = false;
-            break;
-          }
+          wait(cempty_bar(slot), phase ^ 1u, p, kSiteTmaProduced);
           mbar_arrive_expect_tx(cfull_bar(slot), C_BYTES);
           if (GATED) {
             const int32_t out0 = tile.band * HALF + static_cast<int32_t>(rank) * (HALF / 2);
@@ -372,10 +356,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     } else if (warp == 3) {
       // ------------------------------------------------------------------------------ steps and zero points
-      bool ok = true;
       int slot = 0;
       uint32_t phase = 0;
-      for (int t = pair; ok && t < num_tiles; t += n_pairs) {
+      for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
         const Tile tile = tile_at(t);
         int64_t row[4];
 #pragma unroll
@@ -390,10 +373,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           row[i] = (static_cast<int64_t>(tile.e) * p.O + o) * p.G;
         }
         for (int j = 0; j < num_slots; ++j) {
-          if (!dq::warp_wait_any(cempty_bar(slot), phase ^ 1u, st, p.limit_ns, kSiteTmaProduced, false)) {
-            ok = false;
-            break;
-          }
+          wait(cempty_bar(slot), phase ^ 1u, p, kSiteTmaProduced);
+          __syncwarp();
           const int g = 2 * j;
           const uint32_t dst = c_tile(slot) + C_BYTES + static_cast<uint32_t>(lane * 8);
 #pragma unroll
@@ -424,71 +405,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp >= FIRST_DQ) {
     // ------------------------------------------------------------------------------ unpackers
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-    const int set = (warp - FIRST_DQ) / 4;
+    const int set = (warp - FIRST_DQ) / 4;  // which half of every group
     const int quarter = warp & 3;
-    const int r = lane + 32 * quarter;  // the lane's row of the CTA's 128
+    const int r = lane + 32 * quarter;      // the lane's row of the CTA's 128
     const uint32_t sw = static_cast<uint32_t>(r & 7);
-    bool ok = true;
     int slot = 0;
-    uint32_t phase = 0, use = 0;  // k-blocks that this set has filled: buffer set + 2 (use & 1)
-    for (int t = pair; ok && t < num_tiles; t += n_pairs) {
-      for (int j = 0; ok && j < num_slots; ++j) {
-        if (!dq::warp_wait_any(cfull_bar(slot), phase, st, p.limit_ns, kSiteTmaEmpty, false)) {
-          ok = false;
-          break;
-        }
+    uint32_t phase = 0, i = 0;
+    for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
+      for (int g = 0; g < num_groups; ++g, ++i) {
+        const int odd = g & 1;  // a slot's second group
+        if (!odd) wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
         const uint32_t line = c_tile(slot) + static_cast<uint32_t>(r * 128);
-        const uint32_t pa = c_tile(slot) + C_BYTES + P_BYTES + static_cast<uint32_t>(r * 8);
+        const uint32_t chunk = static_cast<uint32_t>(4 * odd + 2 * set);
+        const uint4 w0 = few::lds128(line + ((chunk ^ sw) << 4));
+        const uint4 w1 = few::lds128(line + (((chunk + 1u) ^ sw) << 4));
+        float z;
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(z)
+                     : "r"(c_tile(slot) + C_BYTES + P_BYTES + static_cast<uint32_t>(r * 8 + odd * 4))
+                     : "memory");
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        uint32_t o[32];
+        if (__any_sync(0xffffffffu, !(fabsf(z) <= 240.0f))) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // this set's k-blocks of the slot: set and set + 2, groups 2 j and 2 j + 1
-          const int kb = set + 2 * i;
-          const bool mine = j * SLOT_KB + kb < p.num_kb;  // the last slot may hold one group
-          uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
-          float z = 0.0f;
-          if (mine) {
-            w0 = few::lds128(line + (((2u * kb) ^ sw) << 4));
-            w1 = few::lds128(line + (((2u * kb + 1u) ^ sw) << 4));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(pa + 4u * i) : "memory");
-          }
-          if (i == 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(cempty_bar(slot));
-          }
-          if (!mine) break;
-          const uint32_t buf = static_cast<uint32_t>(set) + 2u * (use & 1u);
-          if (use >= 2 && !dq::warp_wait_any(aempty_bar(static_cast<int>(buf)), ((use >> 1) - 1u) & 1u, st, p.limit_ns,
-                                             kSiteMmaFull, true)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();  // the MMAs that read the buffer come before the stores below
-          ++use;
-          const uint32_t ta = tmem_base + A_COL0 + buf * A_COLS + (static_cast<uint32_t>(quarter * 32) << 16);
-          const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-          uint32_t o[16];
+          for (int c = 0; c < 32; ++c) o[c] = unpack_pair_any((w[c / 4] >> (8 * (c & 3))) & 0xFFu, z);
+        } else {
+          const __nv_bfloat162 zz = __float2bfloat162_rn(z * -0.015625f);
+          const uint32_t zb = *reinterpret_cast<const uint32_t*>(&zz);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (fabsf(z) <= 240.0f) {
-              const __nv_bfloat162 zz = __float2bfloat162_rn(z * -0.015625f);
-              const uint32_t zb = *reinterpret_cast<const uint32_t*>(&zz);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) unpack_word(w[4 * h + c], zb, o + 4 * c);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) o[c] = unpack_pair_any((w[4 * h + c / 4] >> (8 * (c & 3))) & 0xFFu, z);
-            }
-            __syncwarp();
-            tmem_st16(ta + static_cast<uint32_t>(16 * h), o);
-          }
-          tmem_wait_st();
-          tc_fence_before();
+          for (int c = 0; c < 8; ++c) unpack_word(w[c], zb, o + 4 * c);
+        }
+        if (odd || g + 1 == num_groups) {
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(map_to_rank(afull_bar(static_cast<int>(buf)), 0));
+          if (lane == 0) mbar_arrive(cempty_bar(slot));
+          if (++slot == CSTAGES) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
-        if (++slot == CSTAGES) {
-          slot = 0;
-          phase ^= 1u;
-        }
+        if (i >= 2) wait(done_bar(i - 2), parity(i - 2), p, kSiteTmaProduced);
+        __syncwarp();
+        tc_fence_after();  // the MMAs that read the buffer come before the stores below
+        tmem_st32(tmem_base + A_COL0 + (i & 1u) * A_COLS + static_cast<uint32_t>(set * (BK / 2)) +
+                      (static_cast<uint32_t>(quarter * 32) << 16),
+                  o);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(map_to_rank(full_bar(i), 0));
       }
     }
   } else {
@@ -497,9 +461,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, half = (warp - FIRST_EPI) / 4;
     const int r = lane + 32 * quarter;
     int slot = 0;
-    uint32_t phase = 0, group = 0;
-    bool ok = true;
-    for (int t = pair; ok && t < num_tiles; t += n_pairs) {
+    uint32_t phase = 0, i = 0;
+    if (lane == 0) {  // both accumulators are free
+      mbar_arrive_pair(map_to_rank(full_bar(0), 0));
+      mbar_arrive_pair(map_to_rank(full_bar(1), 0));
+    }
+    for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
       const Tile tile = tile_at(t);
       const int chunks = static_cast<int>(tile.n() / 16);
       const int mine = (chunks - half + 1) / 2;  // this warp's blocks: half, half + 2, ...
@@ -509,12 +476,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[c][k] = 0ull;
       float2 steps = make_float2(0.0f, 0.0f);
-      for (int g = 0; g < num_groups; ++g, ++group) {
+      for (int g = 0; g < num_groups; ++g, ++i) {
         if ((g & 1) == 0) {
-          if (!dq::warp_wait_any(cfull_bar(slot), phase, st, p.limit_ns, kSiteTmaEmpty, false)) {
-            ok = false;
-            break;
-          }
+          wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
           steps = few::lds64f(c_tile(slot) + C_BYTES + static_cast<uint32_t>(r * 8));
           __syncwarp();
           if (lane == 0) mbar_arrive(cempty_bar(slot));
@@ -525,13 +489,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         const uint32_t s64 = __float_as_uint(((g & 1) ? steps.y : steps.x) * 64.0f);
         const uint64_t ss = f32x2_pack(s64, s64);
-        const uint32_t acc = group & 1u;
-        if (!dq::warp_wait_any(accf_bar(static_cast<int>(acc)), (group >> 1) & 1u, st, p.limit_ns, kSiteEpiAccFull, false)) {
-          ok = false;
-          break;
-        }
+        wait(done_bar(i), parity(i), p, kSiteEpiAccFull);
+        __syncwarp();
         tc_fence_after();
-        const uint32_t ta = tmem_base + acc * BN + static_cast<uint32_t>(half * 16) + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t ta = tmem_base + (i & 1u) * BN + static_cast<uint32_t>(half * 16) + (static_cast<uint32_t>(quarter * 32) << 16);
         uint32_t v[2][16];
         if (mine > 0) dq::tmem_ld16_issue(ta, v[0]);
 #pragma unroll
@@ -544,9 +505,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_to_rank(acce_bar(static_cast<int>(acc)), 0));
+        if (lane == 0) mbar_arrive_pair(map_to_rank(full_bar(i + 2), 0));  // the group that overwrites it
       }
-      if (!ok) break;
+      if (status_code(st) != 0u) break;  // nothing of an unfinished tile is stored
 
       int64_t o, n_out;
       if (GATED) {
