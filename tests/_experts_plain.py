@@ -54,12 +54,13 @@ def product(X, codes, steps, zeros, rounded_far_zeros=False):
 
 
 def gate(P, err):
-    """silu(a) b of P = [a | b] and the bound after it: |silu'| < 1.1, and the fp32 evaluation off by at most 16
-    roundings."""
+    """silu(a) b of P = [a | b] and the bound after it: |silu'| < 1.1; a fast exponential is off by (2 + 1.2 |a|) units of
+    2^-23 relative (its argument is scaled and rounded), the sum, a fast quotient (2 units) and the product by 4 more; an exponential
+    past the largest float makes 0 of a silu below 2^-120."""
     a, b = P.chunk(2, dim=1)
     ea, eb = err.chunk(2, dim=1)
     s = a / (1 + torch.exp(-a))
-    return s * b, 1.1 * ea * b.abs() + s.abs() * eb + 1.1 * ea * eb + 16 * 2.0 ** -24 * (s * b).abs()
+    return s * b, 1.1 * ea * b.abs() + s.abs() * eb + 1.1 * ea * eb + (6 + 1.2 * a.abs()) * 2.0 ** -23 * (s * b).abs() + 2.0 ** -120 * b.abs()
 
 
 def assert_within(got, ref, err):

@@ -114,7 +114,9 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-__device__ __forceinline__ float silu(float a) { return a / (1.0f + expf(-a)); }
+// a / (1 + exp(-a)) for a result that is rounded to bf16: the fast exponential is off by (2 + |a|) units of 2^-23 and the fast
+// quotient by 2 of its own, a bf16 step is 2^-8.
+__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
 template <bool GATED>
 __global__ void __launch_bounds__(THREADS) w4a16_few_kernel(const Params p) {
