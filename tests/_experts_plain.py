@@ -34,10 +34,12 @@ def dequantized(codes, steps, zeros):
 def product(X, codes, steps, zeros, rounded_far_zeros=False):
     """(X deq(W)^T in 64 bits, bound on a kernel's fp32 error before its output rounding).
 
-    Per group g (A_g = sum of |x| over it): S_g is 128 additions of terms up to 143 |x|, each off by at most one unit
-    2^-23 (the tensor cores may truncate); Sx_g 128 additions in fp32 and its product with 128 + z; the difference and
-    the product with the step one rounding each of values up to (15 + |z|) A_g; the running sums over G groups and
-    up to 8 slices another G + 8 of them. (A kernel that sums q - z itself stays below the same bound.)
+    Per group g (A_g = sum of |x| over it): S_g is 128 additions of terms up to (1024 + 15) |x|, each off by at most one
+    unit 2^-23 (the tensor cores may truncate); the 1024 A_g of the constants are sums of up to 12 levels, and with them
+    subtracted 15 roundings of values up to 1039 A_g; the group's sum of x has 12 more, times |z|; the product with z, the
+    step and the power of two one rounding each of values up to (15 + |z|) A_g; the running sums over G groups and up to 8
+    slices another G + 8 of them. x in fp16 is off by 2^-39 of the group's largest: below one more of those. (A kernel that
+    sums 128 + q or q - z stays below the same bound.)
     rounded_far_zeros: q - z enters rounded to bf16, which is exact up to 256; where |z| > 240 a weight is then off by
     half a bf16 step, 2^-8 of its size."""
     x = X.double()
@@ -45,7 +47,7 @@ def product(X, codes, steps, zeros, rounded_far_zeros=False):
     G = steps.shape[1]
     A = x.abs().view(x.shape[0], G, GROUP).sum(2)
     z = zeros.double().abs()
-    coef = steps.double() * (2 * 128 * 143 + 130 * (128 + z) + (G + 12) * (15 + z))
+    coef = steps.double() * (2 * 128 * 1039 + 15 * 1039 + 12 * z + (G + 12) * (15 + z))
     err = 2.0 ** -24 * (A @ coef.T)
     if rounded_far_zeros:
         far = (z > 240).repeat_interleave(GROUP, 1)

@@ -2,12 +2,16 @@
 // of each expert: Y = X' deq(W)^T, optionally with a bias or with the SiLU gate of a stacked gate and up
 // projection in the epilogue.
 //
-// Mathematics: per group g of 128 in-features, with 128 + q the bf16 pattern 0x4300 | q,
-//   Y[m, o] = sum_g step[o, g] (S_g[o, m] - (128 + z[o, g]) Sx_g[m]),
-//   S_g = sum_{k in g} (128 + q[o, k]) x'[m, k],  Sx_g = sum_{k in g} x'[m, k],
-// so a weight costs one AND-OR per two codes plus a shift, and enters with its exact value; S_g is summed
-// on the tensor cores (m16n8k16, weight rows on the M side, up to 8 tokens on the N side) in fp32, the
-// step and zero point are applied once per group and output in fp32.
+// Mathematics: per group g of 128 in-features and token m, with a power of two c[m, g] that brings the group's largest
+// |x'| to 2^14..2^15 and xs = c x',
+//   Y[m, o] = sum_g step[o, g] / c[m, g] (sum_{k in g} q[o, k] xs[m, k] - z[o, g] sum_{k in g} xs[m, k]).
+// A nibble in place under the exponent bits of 1024 is the fp16 number 1024 + q (bits 0-3) or 1024 + 16 q (bits
+// 4-7), so one AND-OR per two codes and one shift per eight make the operand. In-features of the second kind
+// enter as xs / 16, which makes that operand 64 + q, and what the constants add, 1024 or 64 times sums of xs, is
+// subtracted per group and token. xs is exact in fp16 down to 2^-27 of the group's largest value and below
+// that off by 2^-39 of it, so the weights enter with their exact value; the tensor cores sum in fp32, the
+// step and zero point are applied once per group and output in fp32. (bf16 patterns 128 + q need a shift for
+// every pair of codes: the ALU pipe, at half rate, then took longer than the loads.)
 //
 // The bound is HBM: a weight is read once and used for at most 8 tokens (0.5 byte per 16 operations), so
 // what matters is bytes in flight and few instructions per weight. A one-token product cannot fill the
@@ -25,6 +29,7 @@
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "ptx.cuh"
 
@@ -47,7 +52,7 @@ constexpr int MAX_SLICES = 8;                          // portable cluster size
 
 // Shared memory for chunks of `xg` groups of `mp` tokens (mp = 1, 2, 4 or 8).
 __host__ __device__ constexpr int smem_bytes(int xg, int mp) {
-  return RING_BYTES + PART_BYTES + xg * 256 * mp + xg * TOKENS * 4;
+  return RING_BYTES + PART_BYTES + xg * 256 * mp + xg * TOKENS * 16;
 }
 constexpr int SMEM_MAX = smem_bytes(X_MAX_BYTES / 256, 1);
 static_assert(SMEM_MAX >= smem_bytes(X_MAX_BYTES / 2048, 8), "one token's groups take the most sums");
@@ -98,20 +103,24 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
-// c (16 x 8 fp32) += a (16 x 16 bf16) b (16 x 8 bf16)
+// c (16 x 8 fp32) += a (16 x 16 fp16) b (16 x 8 fp16)
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Codes j and j + 4 of a word as the bf16 pair (128 + q_j, 128 + q_{j+4}).
-template <int J>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  return ((w >> (4 * J)) & 0x000F000Fu) | 0x43004300u;
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
+// Codes 0 and 4 of a word as fp16 (1024 + q); codes 1 and 5 as 1024 + 16 q. The other four: the same of w >> 8.
+__device__ __forceinline__ uint32_t code_even(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }
+__device__ __forceinline__ uint32_t code_odd(uint32_t w) { return (w & 0x00F000F0u) | 0x64006400u; }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 // a / (1 + exp(-a)) for a result that is rounded to bf16: the fast exponential is off by (2 + |a|) units of 2^-23 and the fast
@@ -147,41 +156,48 @@ __global__ void __launch_bounds__(THREADS) w4a16_few_kernel(const Params p) {
   const int n_groups = max(g_end - g_begin, 0);
   const int n_units = (n_groups + UNIT - 1) / UNIT;
 
-  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * DEPTH * STAGE_BYTES);
+  const uint8_t* ring_ptr = smem + warp * DEPTH * STAGE_BYTES;
+  const uint32_t ring = smem_u32(ring_ptr);
   float* part = reinterpret_cast<float*>(smem + RING_BYTES);
   uint8_t* xs = smem + RING_BYTES + PART_BYTES;                      // [group][word][token][t4] 16 bytes
-  float* sx = reinterpret_cast<float*>(xs + (p.xg * 256 << p.mp_log2));  // [group][TOKENS]
-  const uint32_t xs_a = smem_u32(xs), sx_a = smem_u32(sx);
+  // [group][TOKENS]: what the constants add, the sum of xs, 1 / c
+  float4* sx = reinterpret_cast<float4*>(xs + (p.xg * 256 << p.mp_log2));
   const int mp = 1 << p.mp_log2;
 
   const int64_t words = p.K / 8;
-  const uint32_t* code_lo = p.codes + (e * p.O + weight_row(g8)) * words + t4 * 4;
-  const uint32_t* code_hi = p.codes + (e * p.O + weight_row(g8 + 8)) * words + t4 * 4;
-  const float* param = (lane < 16 ? p.steps : p.zeros) + (e * p.O + weight_row(lane & 15)) * p.G;
+  const uint32_t* code_lo = p.codes + (e * p.O + weight_row(g8)) * words + t4 * 4 + g_begin * 16;
+  const uint32_t* code_hi = p.codes + (e * p.O + weight_row(g8 + 8)) * words + t4 * 4 + g_begin * 16;
+  const float* param = (lane < 16 ? p.steps : p.zeros) + (e * p.O + weight_row(lane & 15)) * p.G + g_begin;
 
-  auto issue = [&](int u) {
+  // copies of unit u into the slot at byte `at` of the ring
+  auto issue = [&](int u, uint32_t at) {
     if (u < n_units) {
-      const uint32_t slot = ring + static_cast<uint32_t>((u % DEPTH) * STAGE_BYTES);
-      const int g = g_begin + UNIT * u;
-#pragma unroll
-      for (int i = 0; i < UNIT; ++i)
-        if (g + i < g_end) {
-          cp_async16(slot + static_cast<uint32_t>(i * 1024 + lane * 16), code_lo + (g + i) * 16);
-          cp_async16(slot + static_cast<uint32_t>(i * 1024 + 512 + lane * 16), code_hi + (g + i) * 16);
+      const uint32_t dst = ring + at + static_cast<uint32_t>(lane * 16);
+      const uint32_t* lo = code_lo + u * (UNIT * 16);
+      const uint32_t* hi = code_hi + u * (UNIT * 16);
+      const float* src = param + u * UNIT;
+      const uint32_t pd = ring + at + CODE_BYTES + static_cast<uint32_t>(lane * 8);
+      cp_async16(dst, lo);
+      cp_async16(dst + 512u, hi);
+      if (UNIT * u + 1 < n_groups) {
+        cp_async16(dst + 1024u, lo + 16);
+        cp_async16(dst + 1536u, hi + 16);
+        if (p.pair_params) {
+          cp_async8(pd, src);
+        } else {
+          cp_async4(pd, src);
+          cp_async4(pd + 4u, src + 1);
         }
-      const uint32_t dst = slot + CODE_BYTES + static_cast<uint32_t>(lane * 8);
-      if (p.pair_params) {
-        cp_async8(dst, param + g);
       } else {
-        cp_async4(dst, param + g);
-        if (g + 1 < g_end) cp_async4(dst + 4, param + g + 1);
+        cp_async4(pd, src);
       }
     }
     cp_async_commit();
   };
 
-  // X of tokens m0..m0+mt-1 and groups gc..gc+ng-1, permuted so that one 16-byte piece (in-features 8w..8w+7)
-  // holds the pairs (0, 4), (1, 5), (2, 6), (3, 7), and the sums of each token's groups.
+  // X of tokens m0..m0+mt-1 and groups gc..gc+ng-1 as fp16, scaled and permuted so that one 16-byte piece (in-features
+  // 8w..8w+7) holds the pairs (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16, and the sums of each token's groups. The 16 threads
+  // of a token's group are neighbours.
   auto stage_x = [&](int64_t m0, int mt, int gc, int ng) {
     const int per_token = ng * 16;
     const int total = per_token * mt;
@@ -191,19 +207,32 @@ __global__ void __launch_bounds__(THREADS) w4a16_few_kernel(const Params p) {
       const int m = i / per_token, c = i - m * per_token;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (real) v = *reinterpret_cast<const uint4*>(p.X + (row0 + m0 + m) * p.ldx + static_cast<int64_t>(gc) * 128 + c * 8);
-      float s = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
-                ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t most = 0u;  // exponent bits of the group's largest value
 #pragma unroll
-      for (int d = 1; d < 16; d *= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+      for (int k = 0; k < 4; ++k) most = max(most, max(w[k] & 0x7F80u, (w[k] >> 16) & 0x7F80u));
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+      // c = 2^(14 - exponent), kept below 2^127 so that 1 / c is a normal number
+      const uint32_t field = min(268u - (most >> 7), 253u);
+      const float scale = __uint_as_float(field << 23), back = __uint_as_float((254u - field) << 23);
+      __half2 h[4];  // pairs (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16
+      const float s16 = scale * 0.0625f;
+      h[0] = __floats2half2_rn(bf16_lo(v.x) * scale, bf16_lo(v.z) * scale);
+      h[1] = __floats2half2_rn(bf16_hi(v.x) * s16, bf16_hi(v.z) * s16);
+      h[2] = __floats2half2_rn(bf16_lo(v.y) * scale, bf16_lo(v.w) * scale);
+      h[3] = __floats2half2_rn(bf16_hi(v.y) * s16, bf16_hi(v.w) * s16);
+      const float2 f0 = __half22float2(h[0]), f1 = __half22float2(h[1]), f2 = __half22float2(h[2]), f3 = __half22float2(h[3]);
+      float even = (f0.x + f0.y) + (f2.x + f2.y), odd = 16.0f * ((f1.x + f1.y) + (f3.x + f3.y));
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) {
+        even += __shfl_xor_sync(0xffffffffu, even, d);
+        odd += __shfl_xor_sync(0xffffffffu, odd, d);
+      }
       if (real) {
-        const int grp = c >> 4, t = (c >> 2) & 3, w = c & 3;
-        uint4 q;
-        q.x = __byte_perm(v.x, v.z, 0x5410);  // in-features 0, 4
-        q.y = __byte_perm(v.x, v.z, 0x7632);  // 1, 5
-        q.z = __byte_perm(v.y, v.w, 0x5410);  // 2, 6
-        q.w = __byte_perm(v.y, v.w, 0x7632);  // 3, 7
-        *reinterpret_cast<uint4*>(xs + (((grp * 4 + w) * mp + m) * 4 + t) * 16) = q;
-        if ((c & 15) == 0) sx[grp * TOKENS + m] = s;
+        const int grp = c >> 4, t = (c >> 2) & 3, word = c & 3;
+        *reinterpret_cast<uint4*>(xs + (((grp * 4 + word) * mp + m) * 4 + t) * 16) = *reinterpret_cast<const uint4*>(h);
+        if ((c & 15) == 0) sx[grp * TOKENS + m] = make_float4(fmaf(1024.0f, even, 64.0f * odd), even + odd, back, 0.0f);
       }
     }
   };
@@ -212,9 +241,10 @@ __global__ void __launch_bounds__(THREADS) w4a16_few_kernel(const Params p) {
     const int mt = static_cast<int>(min(rows - m0, static_cast<int64_t>(TOKENS)));
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < DEPTH - 1; ++u) issue(u);
+    for (int u = 0; u < DEPTH - 1; ++u) issue(u, static_cast<uint32_t>(u * STAGE_BYTES));
+    uint32_t at = 0u, ahead = (DEPTH - 1) * STAGE_BYTES;  // slots of unit u and of unit u + DEPTH - 1
     // lanes of tokens past mp read another token's piece: their columns are never stored
-    const uint32_t x_lane = xs_a + static_cast<uint32_t>((((g8 & (mp - 1)) * 4) + t4) * 16);
+    const uint8_t* x_lane = xs + ((((g8 & (mp - 1)) * 4) + t4) * 16);
     int chunk_end = 0, chunk0 = 0;
     for (int u = 0; u < n_units; ++u) {
       if (UNIT * u >= chunk_end) {
@@ -226,32 +256,46 @@ __global__ void __launch_bounds__(THREADS) w4a16_few_kernel(const Params p) {
       }
       cp_async_wait<DEPTH - 2>();
       __syncwarp();  // the stage's steps and zero points, copied by other lanes, and the slot of unit u - 1 read
-      issue(u + DEPTH - 1);
-      const uint32_t slot = ring + static_cast<uint32_t>((u % DEPTH) * STAGE_BYTES);
-      const uint32_t pa = slot + CODE_BYTES + static_cast<uint32_t>(g8 * 8);
-      const float2 st_lo = lds64f(pa), st_hi = lds64f(pa + 64), z_lo = lds64f(pa + 128), z_hi = lds64f(pa + 192);
+      issue(u + DEPTH - 1, ahead);
+      const uint8_t* slot = ring_ptr + at;
+      at = at == (DEPTH - 1) * STAGE_BYTES ? 0u : at + STAGE_BYTES;
+      ahead = ahead == (DEPTH - 1) * STAGE_BYTES ? 0u : ahead + STAGE_BYTES;
+      const float2* pa = reinterpret_cast<const float2*>(slot + CODE_BYTES) + g8;
+      const float2 st_lo = pa[0], st_hi = pa[8], z_lo = pa[16], z_hi = pa[24];
+      // The groups of a unit side by side, in two chains of MMAs each, so that loads, unpacking and MMAs of one hide the
+      // others' latency. A last unit of one group multiplies whatever stands in the slot and drops it.
+      const bool both = UNIT * u + 1 < n_groups;
+      const uint8_t* xu = x_lane + (UNIT * u - chunk0) * (mp * 256);
+      const float4* su = sx + (UNIT * u - chunk0) * TOKENS + 2 * t4;
+      float s[UNIT][2][4];
 #pragma unroll
       for (int i = 0; i < UNIT; ++i) {
-        if (UNIT * u + i < n_groups) {
-          const int gx = UNIT * u + i - chunk0;
-          const uint4 lo = lds128(slot + static_cast<uint32_t>(i * 1024 + lane * 16));
-          const uint4 hi = lds128(slot + static_cast<uint32_t>(i * 1024 + 512 + lane * 16));
-          const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-          float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint4 lo = *reinterpret_cast<const uint4*>(slot + i * 1024 + lane * 16);
+        const uint4 hi = *reinterpret_cast<const uint4*>(slot + i * 1024 + 512 + lane * 16);
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint4 x = lds128(x_lane + static_cast<uint32_t>((gx * 4 + w) * mp * 64));
-            mma16816(s0, code_pair<0>(wl[w]), code_pair<0>(wh[w]), code_pair<1>(wl[w]), code_pair<1>(wh[w]), x.x, x.y);
-            mma16816(s1, code_pair<2>(wl[w]), code_pair<2>(wh[w]), code_pair<3>(wl[w]), code_pair<3>(wh[w]), x.z, x.w);
+        for (int w = 0; w < 4; ++w) {
+          const uint4 x = *reinterpret_cast<const uint4*>(xu + (i * 4 + w) * mp * 64);
+          const uint32_t l8 = wl[w] >> 8, h8 = wh[w] >> 8;
+          if (w == 0) {
+            mma16816_first(s[i][0], code_even(wl[w]), code_even(wh[w]), code_odd(wl[w]), code_odd(wh[w]), x.x, x.y);
+            mma16816_first(s[i][1], code_even(l8), code_even(h8), code_odd(l8), code_odd(h8), x.z, x.w);
+          } else {
+            mma16816(s[i][0], code_even(wl[w]), code_even(wh[w]), code_odd(wl[w]), code_odd(wh[w]), x.x, x.y);
+            mma16816(s[i][1], code_even(l8), code_even(h8), code_odd(l8), code_odd(h8), x.z, x.w);
           }
-          const float2 sums = lds64f(sx_a + static_cast<uint32_t>((gx * TOKENS + 2 * t4) * 4));
-          const float nz_lo = -(128.0f + (i == 0 ? z_lo.x : z_lo.y)), nz_hi = -(128.0f + (i == 0 ? z_hi.x : z_hi.y));
-          const float sl = i == 0 ? st_lo.x : st_lo.y, sh = i == 0 ? st_hi.x : st_hi.y;
-          acc[0] = fmaf(sl, fmaf(nz_lo, sums.x, s0[0] + s1[0]), acc[0]);
-          acc[1] = fmaf(sl, fmaf(nz_lo, sums.y, s0[1] + s1[1]), acc[1]);
-          acc[2] = fmaf(sh, fmaf(nz_hi, sums.x, s0[2] + s1[2]), acc[2]);
-          acc[3] = fmaf(sh, fmaf(nz_hi, sums.y, s0[3] + s1[3]), acc[3]);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < UNIT; ++i) {
+        if (i == 1 && !both) break;
+        const float4 m0s = su[i * TOKENS], m1s = su[i * TOKENS + 1];
+        const float zl = i == 0 ? z_lo.x : z_lo.y, zh = i == 0 ? z_hi.x : z_hi.y;
+        const float sl = i == 0 ? st_lo.x : st_lo.y, sh = i == 0 ? st_hi.x : st_hi.y;
+        acc[0] = fmaf(sl * m0s.z, fmaf(-zl, m0s.y, (s[i][0][0] - m0s.x) + s[i][1][0]), acc[0]);
+        acc[1] = fmaf(sl * m1s.z, fmaf(-zl, m1s.y, (s[i][0][1] - m1s.x) + s[i][1][1]), acc[1]);
+        acc[2] = fmaf(sh * m0s.z, fmaf(-zh, m0s.y, (s[i][0][2] - m0s.x) + s[i][1][2]), acc[2]);
+        acc[3] = fmaf(sh * m1s.z, fmaf(-zh, m1s.y, (s[i][0][3] - m1s.x) + s[i][1][3]), acc[3]);
       }
     }
     cp_async_wait<0>();
