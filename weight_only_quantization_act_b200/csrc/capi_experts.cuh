@@ -40,15 +40,15 @@ awq_status launch_few(awq::few::Params& p, int64_t E, int64_t active, int64_t to
   const int64_t out_rows = gated ? awq::few::ROWS / 2 : awq::few::ROWS;
   const int64_t n_rb = ((gated ? p.O / 2 : p.O) + out_rows - 1) / out_rows;
   if (n_rb > 65535) return fail(AWQ_ERR_INVALID_ARG, "O (%lld) is too large", static_cast<long long>(p.O));
-  // Enough CTAs for two per SM, in slices of at least two groups.
+  // Slices until the CTAs fill the SMs, of at least two groups each.
   int64_t slices = 1;
-  while (slices < awq::few::MAX_SLICES && n_rb * active * slices < 2ll * sms && slices * 2 * awq::few::UNIT <= p.G)
+  while (slices < awq::few::MAX_SLICES && n_rb * active * slices * 2 <= static_cast<int64_t>(awq::few::CTAS_PER_SM) * sms &&
+         slices * 4 <= p.G)
     slices *= 2;
-  p.g_per = static_cast<int>(((p.G + slices - 1) / slices + 1) / 2 * 2);
+  p.g_per = static_cast<int>((p.G + slices - 1) / slices);
   slices = (p.G + p.g_per - 1) / p.g_per;
   p.mp_log2 = tokens <= 1 ? 0 : tokens <= 2 ? 1 : tokens <= 4 ? 2 : 3;
-  p.xg = static_cast<int>(std::min<int64_t>(p.g_per, awq::few::X_MAX_BYTES / (256 << p.mp_log2)));
-  p.pair_params = p.G % 2 == 0 && ((reinterpret_cast<uintptr_t>(p.steps) | reinterpret_cast<uintptr_t>(p.zeros)) & 7u) == 0;
+  p.xg = std::min((p.g_per + awq::few::DEPTH - 1) / awq::few::DEPTH * awq::few::DEPTH, awq::few::chunk_groups(1 << p.mp_log2));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(slices), static_cast<unsigned>(n_rb), static_cast<unsigned>(E));
   cfg.blockDim = dim3(awq::few::THREADS);
@@ -303,7 +303,7 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   q.E = static_cast<int>(E);
   q.min_rows = kFewRows + 1;
   q.n_bands = static_cast<int>(n_bands);
-  q.pair_params = p.pair_params;
+  q.pair_params = q.G % 2 == 0 && ((reinterpret_cast<uintptr_t>(steps) | reinterpret_cast<uintptr_t>(zeros)) & 7u) == 0;
   q.status = static_cast<awq::DeviceStatus*>(workspace);
   q.limit_ns = g_wait_limit_ns.load();
   const unsigned ctas = static_cast<unsigned>(2 * d->expert_clusters);
