@@ -40,11 +40,17 @@ awq_status launch_few(awq::few::Params& p, int64_t E, int64_t active, int64_t to
   const int64_t out_rows = gated ? awq::few::ROWS / 2 : awq::few::ROWS;
   const int64_t n_rb = ((gated ? p.O / 2 : p.O) + out_rows - 1) / out_rows;
   if (n_rb > 65535) return fail(AWQ_ERR_INVALID_ARG, "O (%lld) is too large", static_cast<long long>(p.O));
-  // Slices until the CTAs fill the SMs, of at least two groups each.
-  int64_t slices = 1;
-  while (slices < awq::few::MAX_SLICES && n_rb * active * slices * 2 <= static_cast<int64_t>(awq::few::CTAS_PER_SM) * sms &&
-         slices * 4 <= p.G)
-    slices *= 2;
+  // The number of slices that takes the fewest steps: waves of CTAs times a CTA's groups, and what a CTA does before
+  // and after them, which takes about as long as 10 groups.
+  int64_t slices = 1, best = 0;
+  for (int64_t n = 1; n <= awq::few::MAX_SLICES && 2 * n <= std::max<int64_t>(p.G, 2); ++n) {
+    const int64_t slots = static_cast<int64_t>(awq::few::CTAS_PER_SM) * sms / n * n;
+    const int64_t steps = (n_rb * active * n + slots - 1) / slots * ((p.G + n - 1) / n + 10);
+    if (n == 1 || steps < best) {
+      best = steps;
+      slices = n;
+    }
+  }
   p.g_per = static_cast<int>((p.G + slices - 1) / slices);
   slices = (p.G + p.g_per - 1) / p.g_per;
   p.mp_log2 = tokens <= 1 ? 0 : tokens <= 2 ? 1 : tokens <= 4 ? 2 : 3;

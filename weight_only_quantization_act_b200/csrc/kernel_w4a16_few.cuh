@@ -206,23 +206,25 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
   // 8w..8w+7) holds the pairs (0, 4), (1, 5), (2, 6), (3, 7). The 16 threads of a token's group are neighbours.
   auto stage_x = [&](int64_t m0, int mt, int gc, int ng) {
     const int per_token = ng * 16;
-    const int total = per_token * mt;
     constexpr int AT_ONCE = 4;  // loads in flight per thread
-    for (int base = 0; base < total; base += AT_ONCE * THREADS) {
+    const uint16_t* src = p.X + (row0 + m0) * p.ldx + static_cast<int64_t>(gc) * 128;
+    int m = 0, c = static_cast<int>(threadIdx.x);  // the thread's next token and 16-byte piece
+    while (c >= per_token) c -= per_token, ++m;
+    // all threads of a warp take the same number of turns: its pieces are of neighbouring groups, 16 threads each
+    for (int left = per_token * mt - static_cast<int>(threadIdx.x & ~31u); left > 0; left -= AT_ONCE * THREADS) {
       uint4 v[AT_ONCE];
+      int to[AT_ONCE];
 #pragma unroll
       for (int k = 0; k < AT_ONCE; ++k) {
-        const int i = base + k * THREADS + static_cast<int>(threadIdx.x);
-        const int m = i / per_token, c = i - m * per_token;
         v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < total)
-          v[k] = *reinterpret_cast<const uint4*>(p.X + (row0 + m0 + m) * p.ldx + static_cast<int64_t>(gc) * 128 + c * 8);
+        to[k] = m < mt ? m << 16 | c : -1;
+        if (m < mt) v[k] = *reinterpret_cast<const uint4*>(src + m * p.ldx + c * 8);
+        c += THREADS;
+        while (c >= per_token) c -= per_token, ++m;
       }
 #pragma unroll
       for (int k = 0; k < AT_ONCE; ++k) {
-        if (base + k * THREADS >= total) break;
-        const int i = base + k * THREADS + static_cast<int>(threadIdx.x);
-        const int m = i / per_token, c = i - m * per_token;
+        if (k * THREADS >= left) break;
         // exponent of the group's largest value
         uint32_t most = max(max(exponent_max(v[k].x), exponent_max(v[k].y)), max(exponent_max(v[k].z), exponent_max(v[k].w)));
 #pragma unroll
@@ -235,10 +237,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
         h[1] = __floats2half2_rn(bf16_hi(v[k].x) * scale, bf16_hi(v[k].z) * scale);
         h[2] = __floats2half2_rn(bf16_lo(v[k].y) * scale, bf16_lo(v[k].w) * scale);
         h[3] = __floats2half2_rn(bf16_hi(v[k].y) * scale, bf16_hi(v[k].w) * scale);
-        if (i < total) {
-          const int grp = c >> 4, t = (c >> 2) & 3, word = c & 3;
-          *reinterpret_cast<uint4*>(xs + (((grp * 4 + word) * mp + m) * 4 + t) * 16) = *reinterpret_cast<const uint4*>(h);
-          if ((c & 15) == 0) back[grp * TOKENS + m] = __uint_as_float((254u - field) << 23);
+        if (to[k] >= 0) {
+          const int mk = to[k] >> 16, ck = to[k] & 0xFFFF;
+          const int grp = ck >> 4, t = (ck >> 2) & 3, word = ck & 3;
+          *reinterpret_cast<uint4*>(xs + (((grp * 4 + word) * mp + mk) * 4 + t) * 16) = *reinterpret_cast<const uint4*>(h);
+          if ((ck & 15) == 0) back[grp * TOKENS + mk] = __uint_as_float((254u - field) << 23);
         }
       }
     }
@@ -286,13 +289,26 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
       const int chunk = min(p.xg, n_groups - chunk0);
       __syncthreads();  // the previous chunk has been read
       if (lane < chunk) {  // steps and zero points, a row of this warp's at a time: a row's groups are neighbours
-        const int64_t first = e * p.O * p.G + g_begin + chunk0 + lane;
+        const int64_t first = (e * p.O + weight_row(0)) * p.G + g_begin + chunk0 + lane;
+        const float* ps = p.steps + first;
+        const float* pz = p.zeros + first;
+        const int64_t up = n_out * p.G;                            // gated: from a gate row to its up row
+        int rows_left = static_cast<int>(min(n_out - 1 - weight_row(0), int64_t(32)));  // rows past the end: the last one's
         uint32_t dst = smem_u32(param + lane * PARAM_LD + warp * 32);
 #pragma unroll 4
-        for (int r = 0; r < 32; ++r, dst += 8u) {
-          const int64_t at = first + weight_row(r) * p.G;
-          cp_async4(dst, p.steps + at);
-          cp_async4(dst + 4u, p.zeros + at);
+        for (int r = 0; r < (GATED ? 16 : 32); ++r) {
+          // gated: gate row r is row r % 8 of MMA tile r / 8, its up row 8 behind it
+          const uint32_t to = dst + static_cast<uint32_t>((GATED ? (r >> 3) * 16 + (r & 7) : r) * 8);
+          cp_async4(to, ps);
+          cp_async4(to + 4u, pz);
+          if (GATED) {
+            cp_async4(to + 64u, ps + up);
+            cp_async4(to + 68u, pz + up);
+          }
+          if (--rows_left >= 0) {
+            ps += p.G;
+            pz += p.G;
+          }
         }
       }
       stage_x(m0, mt, g_begin + chunk0, chunk);
