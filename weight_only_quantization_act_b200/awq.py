@@ -449,18 +449,24 @@ def _on_stream(fn):
     @functools.wraps(fn)
     def wrapper(*args, stream=None, **kwargs):
         first = args[0] if args else next(iter(kwargs.values()))
-        device = first.device if isinstance(first, torch.Tensor) and first.is_cuda else None
+        on_cuda = isinstance(first, torch.Tensor) and first.is_cuda
         if stream is not None:
-            if device is not None and stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            if on_cuda and stream.device != first.device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
             with torch.cuda.stream(stream):
                 return fn(*args, **kwargs)
-        if device is None or device.index == torch.cuda.current_device():
+        if not on_cuda or first.get_device() == torch.cuda.current_device():
             return fn(*args, **kwargs)
-        with torch.cuda.device(device):
+        with torch.cuda.device(first.device):
             return fn(*args, **kwargs)
 
     return wrapper
+
+
+def _current_stream() -> int:
+    """Handle of the current stream of the current device (torch.cuda.current_stream builds an object around it, which
+    takes as long as the rest of a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _rows(name: str, t: torch.Tensor, device=None) -> torch.Tensor:
@@ -473,38 +479,38 @@ def _rows(name: str, t: torch.Tensor, device=None) -> torch.Tensor:
 
 def _ld(t: torch.Tensor) -> int:
     """Row stride in elements; a single row's stride does not matter and torch may give any number for it."""
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
 
 
-def _tensor(name: str, t: torch.Tensor, dtypes, shape, device) -> torch.Tensor:
-    """A contiguous argument of one of `dtypes`, of this shape, on `device`."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-        raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
-    if tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+def _tensor(name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """The address of a contiguous argument of this type and shape on `device`."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a tensor of {dtype}")
+    if t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be contiguous, of shape {list(shape)} and on {device}")
-    return t
+    return t.data_ptr()
 
 
-def _rows_out(name: str, out: torch.Tensor | None, rows: int, cols: int, device) -> torch.Tensor:
+def _rows_out(name: str, out: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
     """A bf16 output matrix: a new one, or the caller's."""
     if out is None:
-        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+        return like.new_empty((rows, cols))
     if not isinstance(out, torch.Tensor) or out.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be a bfloat16 tensor")
-    if tuple(out.shape) != (rows, cols) or out.device != device or (cols > 1 and out.stride(1) != 1):
-        raise ValueError(f"{name} must be [{rows}, {cols}] with unit column stride on {device}")
+    if out.shape != (rows, cols) or out.device != like.device or (cols > 1 and out.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}, {cols}] with unit column stride on {like.device}")
     return out
 
 
-def _packed(codes, steps, zeros, lead: tuple, K: int, device) -> int:
-    """Checks packed weights [*lead, O, ...] against X's K in-features; returns O."""
-    if not isinstance(codes, torch.Tensor) or codes.dim() != len(lead) + 1 + 1:
+def _packed(codes, steps, zeros, lead: tuple, K: int, device) -> tuple:
+    """O of packed weights [*lead, O, ...] and their addresses, after checking them against X's K in-features."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != len(lead) + 2:
         raise TypeError(f"codes must be a {len(lead) + 2}-dimensional int32 tensor, as quantize_pack gives it")
     O = codes.shape[-2]
-    _tensor("codes", codes, (torch.int32, torch.uint32), (*lead, O, K // 8), device)
-    _tensor("steps", steps, (torch.float32,), (*lead, O, K // 128), device)
-    _tensor("zeros", zeros, (torch.float32,), (*lead, O, K // 128), device)
-    return O
+    groups = (*lead, O, K // 128)
+    return (O, _tensor("codes", codes, torch.int32, (*lead, O, K // 8), device),
+            _tensor("steps", steps, torch.float32, groups, device), _tensor("zeros", zeros, torch.float32, groups, device))
 
 
 @_on_stream
@@ -516,13 +522,12 @@ def w4a16_gemv(X: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, zeros:
     lib = load_library()
     X = _rows("X", X)
     M, K = X.shape
-    O = _packed(codes, steps, zeros, (), K, X.device)
-    if bias is not None:
-        _tensor("bias", bias, (torch.bfloat16,), (O,), X.device)
-    out = _rows_out("out", out, M, O // 2 if gated else O, X.device)
-    _check("awq_w4a16_gemv", lib.awq_w4a16_gemv(
-        _ptr(X), M, K, _ld(X), _ptr(codes), _ptr(steps), _ptr(zeros), O, None if bias is None else _ptr(bias),
-        int(gated), _ptr(out), out.stride(0), _stream(None)))
+    device = X.device
+    O, c, s, z = _packed(codes, steps, zeros, (), K, device)
+    bias = None if bias is None else _tensor("bias", bias, torch.bfloat16, (O,), device)
+    out = _rows_out("out", out, M, O // 2 if gated else O, X)
+    _check("awq_w4a16_gemv", lib.awq_w4a16_gemv(X.data_ptr(), M, K, _ld(X), c, s, z, O, bias, bool(gated), out.data_ptr(),
+                                                out.stride(0), _current_stream()))
     return out
 
 
@@ -537,15 +542,14 @@ class ExpertSort:
     pos: torch.Tensor
 
     def checked(self, device) -> tuple:
-        """(T, k, E) after checking the three tensors against each other."""
+        """(T, k, E) and the addresses of offsets, order and pos, after checking the three against each other."""
         if not isinstance(self.pos, torch.Tensor) or self.pos.dim() != 2 or self.offsets.dim() != 1:
             raise TypeError("an ExpertSort holds offsets [E + 1], order [T * k] and pos [T, k]")
         T, k = self.pos.shape
         E = self.offsets.shape[0] - 1
-        _tensor("pos", self.pos, (torch.int32,), (T, k), device)
-        _tensor("order", self.order, (torch.int32,), (T * k,), device)
-        _tensor("offsets", self.offsets, (torch.int32,), (E + 1,), device)
-        return T, k, E
+        return (T, k, E, _tensor("offsets", self.offsets, torch.int32, (E + 1,), device),
+                _tensor("order", self.order, torch.int32, (T * k,), device),
+                _tensor("pos", self.pos, torch.int32, (T, k), device))
 
 
 @_on_stream
@@ -557,19 +561,19 @@ def expert_sort(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor | Non
         raise TypeError("ids must be a CUDA int32 or int64 matrix [tokens, picks]")
     ids = ids.contiguous()
     n = ids.numel()
-    offsets = torch.empty(n_experts + 1 if n_experts >= 0 else 1, dtype=torch.int32, device=ids.device)
-    order = torch.empty(n, dtype=torch.int32, device=ids.device)
-    pos = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+    offsets = ids.new_empty(max(n_experts, 0) + 1, dtype=torch.int32)
+    order = ids.new_empty(n, dtype=torch.int32)
+    pos = ids.new_empty(ids.shape, dtype=torch.int32)
     need = lib.awq_expert_sort_workspace_size(n, n_experts)
     ws = _workspace(need, ids.device, workspace) if need else None
     _check("awq_expert_sort", lib.awq_expert_sort(
-        _ptr(ids), ids.element_size(), n, n_experts, _ptr(ws) if need else None, need, _ptr(offsets), _ptr(order),
-        _ptr(pos), _stream(None)))
+        ids.data_ptr(), ids.element_size(), n, n_experts, ws.data_ptr() if need else None, need, offsets.data_ptr(),
+        order.data_ptr(), pos.data_ptr(), _current_stream()))
     return ExpertSort(offsets, order, pos)
 
 
 def _scales(scales, E: int, K: int, device):
-    return None if scales is None else _ptr(_tensor("scales", scales, (torch.float32,), (E, K), device))
+    return None if scales is None else _tensor("scales", scales, torch.float32, (E, K), device)
 
 
 @_on_stream
@@ -579,14 +583,14 @@ def expert_gather(X: torch.Tensor, sort: ExpertSort, scales: torch.Tensor | None
     scales, as scale_columns(divide=True) does. Rows behind the last routed one are not written."""
     lib = load_library()
     X = _rows("X", X)
-    T, k, E = sort.checked(X.device)
+    T, k, E, offsets, order, _ = sort.checked(X.device)
     K = X.shape[1]
     if X.shape[0] != T:
         raise ValueError(f"X has {X.shape[0]} rows, the sort {T} tokens")
-    out = _rows_out("out", out, T * k, K, X.device)
+    out = _rows_out("out", out, T * k, K, X)
     _check("awq_expert_gather", lib.awq_expert_gather(
-        _ptr(X), T, K, _ld(X), k, _ptr(sort.offsets), E, _ptr(sort.order), _scales(scales, E, K, X.device), _ptr(out),
-        _ld(out), _stream(None)))
+        X.data_ptr(), T, K, _ld(X), k, offsets, E, order, _scales(scales, E, K, X.device), out.data_ptr(), _ld(out),
+        _current_stream()))
     return out
 
 
@@ -596,14 +600,14 @@ def expert_gather_backward(dXs: torch.Tensor, sort: ExpertSort, scales: torch.Te
     """Gradient of expert_gather: dX[t] = the sum of its rows of dXs (each divided by its expert's scales)."""
     lib = load_library()
     dXs = _rows("dXs", dXs)
-    T, k, E = sort.checked(dXs.device)
+    T, k, E, offsets, _, pos = sort.checked(dXs.device)
     K = dXs.shape[1]
     if dXs.shape[0] != T * k:
         raise ValueError(f"dXs has {dXs.shape[0]} rows, the sort {T * k}")
-    out = _rows_out("out", out, T, K, dXs.device)
+    out = _rows_out("out", out, T, K, dXs)
     _check("awq_expert_gather_backward", lib.awq_expert_gather_backward(
-        _ptr(dXs), T, K, _ld(dXs), k, _ptr(sort.offsets), E, _ptr(sort.pos), _scales(scales, E, K, dXs.device),
-        _ptr(out), _ld(out), _stream(None)))
+        dXs.data_ptr(), T, K, _ld(dXs), k, offsets, E, pos, _scales(scales, E, K, dXs.device), out.data_ptr(), _ld(out),
+        _current_stream()))
     return out
 
 
@@ -613,14 +617,14 @@ def expert_combine(Ys: torch.Tensor, sort: ExpertSort, weights: torch.Tensor | N
     """Y[t] = sum_j weights[t, j] * Ys[pos[t, j]] (bf16 [T, O], fp32 sums; weights float32 [T, k], ones if None)."""
     lib = load_library()
     Ys = _rows("Ys", Ys)
-    T, k, _ = sort.checked(Ys.device)
+    T, k, _, _, _, pos = sort.checked(Ys.device)
     O = Ys.shape[1]
     if Ys.shape[0] != T * k:
         raise ValueError(f"Ys has {Ys.shape[0]} rows, the sort {T * k}")
-    w = None if weights is None else _ptr(_tensor("weights", weights, (torch.float32,), (T, k), Ys.device))
-    out = _rows_out("out", out, T, O, Ys.device)
+    w = None if weights is None else _tensor("weights", weights, torch.float32, (T, k), Ys.device)
+    out = _rows_out("out", out, T, O, Ys)
     _check("awq_expert_combine", lib.awq_expert_combine(
-        _ptr(Ys), T, O, _ld(Ys), k, _ptr(sort.pos), w, _ptr(out), _ld(out), _stream(None)))
+        Ys.data_ptr(), T, O, _ld(Ys), k, pos, w, out.data_ptr(), _ld(out), _current_stream()))
     return out
 
 
@@ -632,16 +636,16 @@ def expert_combine_backward(dY: torch.Tensor, Ys: torch.Tensor, sort: ExpertSort
     lib = load_library()
     dY = _rows("dY", dY)
     Ys = _rows("Ys", Ys, dY.device)
-    T, k, _ = sort.checked(dY.device)
+    T, k, _, _, _, pos = sort.checked(dY.device)
     O = dY.shape[1]
     if dY.shape[0] != T or tuple(Ys.shape) != (T * k, O):
         raise ValueError(f"dY {list(dY.shape)} and Ys {list(Ys.shape)} do not fit a sort of {T} tokens, {k} picks")
-    _tensor("weights", weights, (torch.float32,), (T, k), dY.device)
-    out = _rows_out("out", out, T * k, O, dY.device)
-    dweights = torch.empty((T, k), dtype=torch.float32, device=dY.device)
+    w = _tensor("weights", weights, torch.float32, (T, k), dY.device)
+    out = _rows_out("out", out, T * k, O, dY)
+    dweights = weights.new_empty((T, k))
     _check("awq_expert_combine_backward", lib.awq_expert_combine_backward(
-        _ptr(dY), T, O, _ld(dY), _ptr(Ys), _ld(Ys), k, _ptr(sort.pos), _ptr(weights), _ptr(out), _ld(out),
-        _ptr(dweights), _stream(None)))
+        dY.data_ptr(), T, O, _ld(dY), Ys.data_ptr(), _ld(Ys), k, pos, w, out.data_ptr(), _ld(out), dweights.data_ptr(),
+        _current_stream()))
     return out, dweights
 
 
@@ -665,14 +669,14 @@ def w4a16_experts(Xs: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor, 
     Xs = _rows("Xs", Xs)
     R, K = Xs.shape
     E = codes.shape[0]
-    O = _packed(codes, steps, zeros, (E,), K, Xs.device)
-    _tensor("offsets", offsets, (torch.int32,), (E + 1,), Xs.device)
-    out = _rows_out("out", out, R, O // 2 if gated else O, Xs.device)
+    O, c, s, z = _packed(codes, steps, zeros, (E,), K, Xs.device)
+    first = _tensor("offsets", offsets, torch.int32, (E + 1,), Xs.device)
+    out = _rows_out("out", out, R, O // 2 if gated else O, Xs)
     if workspace is None:
         workspace = w4a16_experts_workspace(codes, R)
     _check("awq_w4a16_experts", lib.awq_w4a16_experts(
-        _ptr(Xs), R, K, _ld(Xs), _ptr(offsets), E, _ptr(codes), _ptr(steps), _ptr(zeros), O, int(gated), _ptr(out),
-        out.stride(0), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(None)))
+        Xs.data_ptr(), R, K, _ld(Xs), first, E, c, s, z, O, bool(gated), out.data_ptr(), out.stride(0), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _current_stream()))
     return out
 
 

@@ -367,11 +367,18 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
       mine[(2 * t4) * PART_LD + 8] = acc[i][2];
       mine[(2 * t4 + 1) * PART_LD + 8] = acc[i][3];
     }
-    cluster_sync();
+    if (slices > 1) cluster_sync();
+    else __syncthreads();
     const uint32_t part_a = smem_u32(part);
     auto total = [&](int idx) {
+      if (slices == 1) return part[idx];
+      float from[MAX_SLICES];  // all of them on their way before the first is added
+#pragma unroll
+      for (int r = 0; r < MAX_SLICES; ++r)
+        from[r] = r < slices ? ld_cluster_f32(map_to_rank(part_a + static_cast<uint32_t>(idx * 4), r)) : 0.0f;
       float v = 0.0f;
-      for (int r = 0; r < slices; ++r) v += ld_cluster_f32(map_to_rank(part_a + static_cast<uint32_t>(idx * 4), r));
+#pragma unroll
+      for (int r = 0; r < MAX_SLICES; ++r) v += from[r];
       return v;
     };
     const int share = (OUT_ROWS + slices - 1) / slices;
@@ -393,7 +400,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
       const __nv_bfloat16 y = __float2bfloat16_rn(v);
       p.Y[(row0 + m0 + m) * p.ldy + o] = *reinterpret_cast<const uint16_t*>(&y);
     }
-    cluster_sync();  // every CTA has read this one's partial sums
+    if (slices > 1) cluster_sync();  // every CTA has read this one's partial sums
+    else __syncthreads();
   }
 }
 
