@@ -119,7 +119,15 @@ awq_status check_rows_args(int64_t T, int64_t top_k, int64_t K) {
   if (T >= (1ll << 31) || top_k >= (1ll << 31) || T * top_k >= (1ll << 31))
     return fail(AWQ_ERR_INVALID_ARG, "too many slots");
   if (K % 8 != 0) return fail(AWQ_ERR_INVALID_ARG, "K (%lld) must be a multiple of 8", static_cast<long long>(K));
+  if (K > 65535ll * 8 * awq::ex::ROW_THREADS)  // the grid's y extent
+    return fail(AWQ_ERR_INVALID_ARG, "K (%lld) is too large", static_cast<long long>(K));
   return AWQ_OK;
+}
+
+// Blocks along the columns where a thread takes `pieces` of 8 columns.
+unsigned column_blocks(int64_t K, int pieces) {
+  const int64_t per_block = 8ll * awq::ex::ROW_THREADS * pieces;
+  return static_cast<unsigned>((K + per_block - 1) / per_block);
 }
 
 template <typename ID>
@@ -184,10 +192,17 @@ extern "C" awq_status awq_expert_gather(const void* X, int64_t T, int64_t K, int
   if (!aligned16(scales)) return fail(AWQ_ERR_INVALID_ARG, "scales is not 16-byte aligned");
   DeviceInfo* d = nullptr;
   AWQ_TRY(device_info(&d));
-  awq::ex::expert_gather_kernel<<<static_cast<unsigned>(T * top_k), awq::ex::ROW_THREADS, 0,
-                                  reinterpret_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint16_t*>(X), ldx, T, K, offsets, static_cast<int>(E), order, static_cast<int>(top_k), scales,
-      static_cast<uint16_t*>(Xs), ldxs);
+  const int64_t n = T * top_k;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (scales == nullptr) {
+    awq::ex::expert_gather_kernel<<<static_cast<unsigned>(n), awq::ex::ROW_THREADS, 0, st>>>(
+        static_cast<const uint16_t*>(X), ldx, T, K, order, static_cast<int>(top_k), static_cast<uint16_t*>(Xs), ldxs);
+  } else {
+    const dim3 grid(static_cast<unsigned>((n + awq::ex::RUN - 1) / awq::ex::RUN), column_blocks(K, 1));
+    awq::ex::expert_gather_scaled_kernel<<<grid, awq::ex::ROW_THREADS, 0, st>>>(
+        static_cast<const uint16_t*>(X), ldx, T, K, offsets, static_cast<int>(E), order, static_cast<int>(top_k), scales,
+        static_cast<uint16_t*>(Xs), ldxs, n);
+  }
   AWQ_TRY(check_launch("expert_gather_kernel"));
   return ok();
 }
@@ -198,10 +213,18 @@ awq_status combine(const void* Ys, int64_t T, int64_t K, int64_t ldys, int64_t t
                    awq_stream_t stream) {
   DeviceInfo* d = nullptr;
   AWQ_TRY(device_info(&d));
-  awq::ex::expert_combine_kernel<<<static_cast<unsigned>(T), awq::ex::ROW_THREADS, 0,
-                                   reinterpret_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint16_t*>(Ys), ldys, K, pos, static_cast<int>(top_k), T * top_k, weights, offsets,
-      static_cast<int>(E), scales, static_cast<uint16_t*>(Y), ldy);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (scales == nullptr) {
+    const dim3 grid(static_cast<unsigned>(T), column_blocks(K, 2));
+    awq::ex::expert_combine_kernel<<<grid, awq::ex::ROW_THREADS, 0, st>>>(
+        static_cast<const uint16_t*>(Ys), ldys, K, pos, static_cast<int>(top_k), T * top_k, weights,
+        static_cast<uint16_t*>(Y), ldy);
+  } else {
+    const dim3 grid(static_cast<unsigned>(T), column_blocks(K, 1));
+    awq::ex::expert_combine_scaled_kernel<<<grid, awq::ex::ROW_THREADS, 0, st>>>(
+        static_cast<const uint16_t*>(Ys), ldys, K, pos, static_cast<int>(top_k), T * top_k, offsets, static_cast<int>(E),
+        scales, static_cast<uint16_t*>(Y), ldy);
+  }
   AWQ_TRY(check_launch("expert_combine_kernel"));
   return ok();
 }

@@ -206,61 +206,187 @@ __device__ __forceinline__ int expert_of_row(const int* __restrict__ offsets, in
   return lo;
 }
 
-constexpr int ROW_THREADS = 256;
+// The row kernels are bound by HBM: a thread keeps several 16-byte loads in flight, the threads of a block neighbours.
+constexpr int ROW_THREADS = 128;
+constexpr int AT_ONCE = 4;                                       // 16-byte pieces of a row per thread and turn
+constexpr int ROW_PIECES = ROW_THREADS * AT_ONCE;                // 4096 columns a turn
 
-// Xs[r] = X[order[r] / top_k] (/ scales[expert of r]): one row per block, 16 bytes per thread and step.
+__device__ __forceinline__ uint4 ld_row(const uint16_t* row, int64_t piece) {
+  return __ldg(reinterpret_cast<const uint4*>(row) + piece);
+}
+
+// Xs[r] = X[order[r] / top_k]: a row per block.
 __global__ void __launch_bounds__(ROW_THREADS) expert_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t T,
-                                                                    int64_t K, const int* __restrict__ offsets, int E,
-                                                                    const int* __restrict__ order, int top_k,
-                                                                    const float* __restrict__ scales,
+                                                                    int64_t K, const int* __restrict__ order, int top_k,
                                                                     uint16_t* __restrict__ Xs, int64_t ldxs) {
   const int64_t r = blockIdx.x;
   const int slot = order[r];
   if (slot < 0 || slot >= T * top_k) return;
-  const uint4* src = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(slot / top_k) * ldx);
+  const uint16_t* src = X + static_cast<int64_t>(slot / top_k) * ldx;
   uint4* dst = reinterpret_cast<uint4*>(Xs + r * ldxs);
-  const float* sc = scales == nullptr ? nullptr : scales + expert_of_row(offsets, E, static_cast<int>(r)) * K;
-  for (int64_t c = threadIdx.x; c < K / 8; c += ROW_THREADS) {
-    uint4 v = src[c];
-    if (sc != nullptr) {
-      float f[8];
-      unpack8(v, f);
+  const int64_t pieces = K / 8;
+  for (int64_t c = threadIdx.x; c < pieces; c += ROW_PIECES) {
+    uint4 v[AT_ONCE];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], sc[c * 8 + i]);
-      v = pack8(f);
-    }
-    dst[c] = v;
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (c + i * ROW_THREADS < pieces) v[i] = ld_row(src, c + i * ROW_THREADS);
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (c + i * ROW_THREADS < pieces) dst[c + i * ROW_THREADS] = v[i];
   }
 }
 
-// Y[t] = sum over token t's routed slots, in slot order, of weight * Ys[pos] (or Ys[pos] / scales[expert]), in fp32.
+// bf16(RN32(x / s)) with r = RN32(1 / s): x r is within three units of the last place of RN32(x / s) while both are normal numbers, so
+// its rounding to bf16 is the same unless it lies that near the middle between two bf16 numbers (`near`, then the
+// division decides; 1 of 7000).
+__device__ __forceinline__ float quotient_fast(float x, float r, bool& near) {
+  const float q = __fmul_rn(x, r);
+  const uint32_t bits = __float_as_uint(q);
+  const uint32_t exponent = (bits >> 23) & 0xFFu;
+  near |= (bits & 0xFFFFu) - 0x7FFCu <= 8u || (exponent - 2u > 250u && x != 0.0f);
+  return q;
+}
+
+// Xs[r] = X[order[r] / top_k] / scales[expert of r]: a block takes a run of sorted rows, most of them of one expert, and 1024
+// columns, so a thread reads its 8 scales and their reciprocals once per expert and not once per row (the scales of a row
+// are twice its bytes).
+constexpr int RUN = 16;
+__global__ void __launch_bounds__(ROW_THREADS) expert_gather_scaled_kernel(
+    const uint16_t* __restrict__ X, int64_t ldx, int64_t T, int64_t K, const int* __restrict__ offsets, int E,
+    const int* __restrict__ order, int top_k, const float* __restrict__ scales, uint16_t* __restrict__ Xs, int64_t ldxs,
+    int64_t n_rows) {
+  __shared__ int slots[RUN], experts[RUN];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * RUN;
+  if (threadIdx.x < RUN) {
+    const int64_t r = r0 + threadIdx.x;
+    int slot = r < n_rows ? order[r] : -1;
+    if (slot >= T * top_k) slot = -1;
+    slots[threadIdx.x] = slot;
+    experts[threadIdx.x] = slot >= 0 ? expert_of_row(offsets, E, static_cast<int>(r)) : -1;
+  }
+  __syncthreads();
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * ROW_THREADS + threadIdx.x;
+  if (c >= K / 8) return;
+  float s[8], rcp[8];
+  bool odd_scales = false;  // a scale whose reciprocal is no normal number: every row by division
+  int have = -1;
+#pragma unroll 1
+  for (int i0 = 0; i0 < RUN; i0 += AT_ONCE) {
+    uint4 v[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (slots[i0 + i] >= 0) v[i] = ld_row(X + static_cast<int64_t>(slots[i0 + i] / top_k) * ldx, c);
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      if (slots[i0 + i] < 0) continue;
+      const int e = experts[i0 + i];
+      if (e != have) {
+        have = e;
+        const float4* sc = reinterpret_cast<const float4*>(scales + e * K + c * 8);
+        const float4 lo = __ldg(sc), hi = __ldg(sc + 1);
+        s[0] = lo.x; s[1] = lo.y; s[2] = lo.z; s[3] = lo.w; s[4] = hi.x; s[5] = hi.y; s[6] = hi.z; s[7] = hi.w;
+        odd_scales = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          rcp[k] = __fdiv_rn(1.0f, s[k]);
+          const float size = fabsf(rcp[k]);
+          odd_scales |= !(size >= 1.17549435e-38f && size <= 3.0e38f);
+        }
+      }
+      float f[8], q[8];
+      unpack8(v[i], f);
+      bool near = odd_scales;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[k] = quotient_fast(f[k], rcp[k], near);
+      if (near) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = __fdiv_rn(f[k], s[k]);
+      }
+      *reinterpret_cast<uint4*>(Xs + (r0 + i0 + i) * ldxs + c * 8) = pack8(q);
+    }
+  }
+}
+
+// Y[t] = sum over token t's routed slots, in slot order, of weight * Ys[pos], in fp32: a token per block, the rows of four
+// slots on their way at once.
 __global__ void __launch_bounds__(ROW_THREADS) expert_combine_kernel(const uint16_t* __restrict__ Ys, int64_t ldys, int64_t K,
                                                                      const int* __restrict__ pos, int top_k, int64_t n_rows,
                                                                      const float* __restrict__ weights,
-                                                                     const int* __restrict__ offsets, int E,
-                                                                     const float* __restrict__ scales,
                                                                      uint16_t* __restrict__ Y, int64_t ldy) {
-  const int64_t t = blockIdx.x;
-  for (int64_t c = threadIdx.x; c < K / 8; c += ROW_THREADS) {
-    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < top_k; ++j) {
-      const int64_t s = t * top_k + j;
-      const int row = pos[s];
-      if (row < 0 || row >= n_rows) continue;
-      float f[8];
-      unpack8(*reinterpret_cast<const uint4*>(Ys + row * ldys + c * 8), f);
-      if (scales != nullptr) {
-        const float* sc = scales + expert_of_row(offsets, E, row) * K + c * 8;
+  constexpr int SLOTS = 4, PIECES = 2;
+  const int64_t t = blockIdx.x, pieces = K / 8;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (ROW_THREADS * PIECES) + threadIdx.x;
+  float acc[PIECES][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += __fdiv_rn(f[i], sc[i]);
-      } else {
-        const float w = weights == nullptr ? 1.0f : weights[s];
+  for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
-      }
+    for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
+  for (int j0 = 0; j0 < top_k; j0 += SLOTS) {
+    int row[SLOTS];
+    float w[SLOTS];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+      const int64_t s = t * top_k + j0 + j;
+      row[j] = j0 + j < top_k ? __ldg(pos + s) : -1;
+      if (row[j] >= n_rows) row[j] = -1;
+      w[j] = weights != nullptr && j0 + j < top_k ? __ldg(weights + s) : 1.0f;
     }
-    *reinterpret_cast<uint4*>(Y + t * ldy + c * 8) = pack8(acc);
+    uint4 v[SLOTS][PIECES];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i)
+        if (row[j] >= 0 && c0 + i * ROW_THREADS < pieces) v[j][i] = ld_row(Ys + row[j] * ldys, c0 + i * ROW_THREADS);
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i)
+        if (row[j] >= 0 && c0 + i * ROW_THREADS < pieces) {
+          float f[8];
+          unpack8(v[j][i], f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[i][k] = fmaf(w[j], f[k], acc[i][k]);
+        }
   }
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i)
+    if (c0 + i * ROW_THREADS < pieces)
+      reinterpret_cast<uint4*>(Y + t * ldy)[c0 + i * ROW_THREADS] = pack8(acc[i]);
+}
+
+// The same with Ys[pos] / scales[expert] for weight * Ys[pos]: the gradient of the scaled gather.
+__global__ void __launch_bounds__(ROW_THREADS) expert_combine_scaled_kernel(
+    const uint16_t* __restrict__ Ys, int64_t ldys, int64_t K, const int* __restrict__ pos, int top_k, int64_t n_rows,
+    const int* __restrict__ offsets, int E, const float* __restrict__ scales, uint16_t* __restrict__ Y, int64_t ldy) {
+  __shared__ int rows[ROW_THREADS], experts[ROW_THREADS];
+  const int64_t t = blockIdx.x;
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * ROW_THREADS + threadIdx.x;
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j0 = 0; j0 < top_k; j0 += ROW_THREADS) {
+    const int n = min(top_k - j0, ROW_THREADS);
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < n) {
+      const int row = pos[t * top_k + j0 + threadIdx.x];
+      const bool real = row >= 0 && row < n_rows;
+      rows[threadIdx.x] = real ? row : -1;
+      experts[threadIdx.x] = real ? expert_of_row(offsets, E, row) : -1;
+    }
+    __syncthreads();
+    if (c >= K / 8) continue;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      if (rows[j] < 0) continue;
+      float f[8];
+      unpack8(ld_row(Ys + rows[j] * ldys, c), f);
+      const float4* sc = reinterpret_cast<const float4*>(scales + experts[j] * K + c * 8);
+      const float4 lo = __ldg(sc), hi = __ldg(sc + 1);
+      acc[0] += __fdiv_rn(f[0], lo.x); acc[1] += __fdiv_rn(f[1], lo.y);
+      acc[2] += __fdiv_rn(f[2], lo.z); acc[3] += __fdiv_rn(f[3], lo.w);
+      acc[4] += __fdiv_rn(f[4], hi.x); acc[5] += __fdiv_rn(f[5], hi.y);
+      acc[6] += __fdiv_rn(f[6], hi.z); acc[7] += __fdiv_rn(f[7], hi.w);
+    }
+  }
+  if (c < K / 8) reinterpret_cast<uint4*>(Y + t * ldy)[c] = pack8(acc);
 }
 
 // dYs[pos] = weight * dY[t], dweights = <dY[t], Ys[pos]> in fp32 (fixed order: a thread's columns in order, then
@@ -270,24 +396,38 @@ __global__ void __launch_bounds__(ROW_THREADS) expert_combine_backward_kernel(
     const int* __restrict__ pos, int top_k, int64_t n_rows, const float* __restrict__ weights, uint16_t* __restrict__ dYs,
     int64_t lddys, float* __restrict__ dweights) {
   __shared__ float sums[ROW_THREADS / 32];
-  const int64_t s = blockIdx.x, t = s / top_k;
+  const int64_t s = blockIdx.x, t = s / top_k, pieces = K / 8;
   const int row = pos[s];
   if (row < 0 || row >= n_rows) {
     if (threadIdx.x == 0) dweights[s] = 0.0f;
     return;
   }
   const float w = weights[s];
+  const uint16_t* g_row = dY + t * lddy;
+  const uint16_t* y_row = Ys + row * ldys;
+  uint4* dst = reinterpret_cast<uint4*>(dYs + row * lddys);
   float dot = 0.0f;
-  for (int64_t c = threadIdx.x; c < K / 8; c += ROW_THREADS) {
-    float g[8], y[8];
-    unpack8(*reinterpret_cast<const uint4*>(dY + t * lddy + c * 8), g);
-    unpack8(*reinterpret_cast<const uint4*>(Ys + row * ldys + c * 8), y);
+  for (int64_t c = threadIdx.x; c < pieces; c += ROW_PIECES) {
+    uint4 vg[AT_ONCE], vy[AT_ONCE];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dot = fmaf(g[i], y[i], dot);
-      g[i] *= w;
-    }
-    *reinterpret_cast<uint4*>(dYs + row * lddys + c * 8) = pack8(g);
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (c + i * ROW_THREADS < pieces) {
+        vy[i] = ld_row(y_row, c + i * ROW_THREADS);
+        vg[i] = ld_row(g_row, c + i * ROW_THREADS);
+      }
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (c + i * ROW_THREADS < pieces) {
+        float g[8], y[8];
+        unpack8(vg[i], g);
+        unpack8(vy[i], y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          dot = fmaf(g[k], y[k], dot);
+          g[k] *= w;
+        }
+        dst[c + i * ROW_THREADS] = pack8(g);
+      }
   }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, d);
