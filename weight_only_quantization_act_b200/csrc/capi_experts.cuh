@@ -110,7 +110,7 @@ extern "C" awq_status awq_w4a16_gemv(const void* X, int64_t M, int64_t K, int64_
 // ------------------------------------------------------------------------------------------- expert sort
 namespace {
 int64_t sort_blocks(int64_t n) {
-  if (n <= awq::ex::SORT_TILE) return 1;  // one block counts and places
+  if (n <= awq::ex::SORT_ALONE) return 1;  // one block counts and places
   return std::min<int64_t>((n + 1023) / 1024, awq::ex::SORT_MAX_BLOCKS);
 }
 

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 
+#include "dequant_w4.cuh"
 #include "ptx.cuh"
 
 namespace awq {
@@ -16,8 +17,8 @@ namespace ex {
 
 constexpr int SORT_THREADS = 256;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_ITERS = 16;                                   // slots per lane and tile
-constexpr int SORT_TILE = SORT_THREADS * SORT_ITERS;             // 4096 slots: one CTA sorts these alone
+constexpr int SORT_ITERS = 16;                                   // slots per lane and tile at most
+constexpr int SORT_ALONE = SORT_THREADS * SORT_ITERS;            // 4096 slots: one CTA sorts these alone
 constexpr int MAX_EXPERTS = 1024;
 constexpr int SORT_MAX_BLOCKS = 256;
 
@@ -78,8 +79,8 @@ __device__ __forceinline__ int block_scan(int* v, int E, int* warp_sums) {
 }
 
 // Stable counting sort. Block b places its slots; with counts == nullptr there is one block, which counts
-// for itself. Inside a block the slots are taken in tiles of 4096; each warp takes 512 consecutive slots of
-// the tile, 32 at a time, and a lane's rank among equal picks is the popcount of the match mask below it
+// for itself. Inside a block the slots are taken in tiles of up to 4096; each warp takes an eighth of the tile, consecutive
+// slots, 32 at a time, and a lane's rank among equal picks is the popcount of the match mask below it
 // plus the warp's running count, so equal picks keep the order of their slots.
 template <typename ID>
 __global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const ID* __restrict__ ids, int64_t n, int E,
@@ -93,21 +94,21 @@ __global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const ID* __
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t begin = blockIdx.x * per_block, end = min(begin + per_block, n);
 
-  int before[MAX_EXPERTS / SORT_THREADS];
+  // all[e] over the blocks, into base, and before[e] over those before this one, into whist's first row: a warp takes every
+  // eighth block's counts, 32 experts at a time
   if (counts != nullptr) {
-#pragma unroll
-    for (int i = 0; i < MAX_EXPERTS / SORT_THREADS; ++i) {
-      const int e = threadIdx.x + i * SORT_THREADS;
-      before[i] = 0;
-      if (e < E) {
-        int all = 0;
-        for (unsigned b = 0; b < gridDim.x; ++b) {
-          const int c = counts[static_cast<int64_t>(b) * E + e];
-          if (b < blockIdx.x) before[i] += c;
-          all += c;
-        }
-        base[e] = all;
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) base[e] = whist[e] = 0;
+    __syncthreads();
+    for (int e = lane; e < E; e += 32) {
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (unsigned b = warp; b < gridDim.x; b += SORT_WARPS) {
+        const int c = counts[static_cast<int64_t>(b) * E + e];
+        all += c;
+        before += b < blockIdx.x ? c : 0;
       }
+      if (all != 0) atomicAdd(&base[e], all);  // counts: the order of the additions does not show
+      if (before != 0) atomicAdd(&whist[e], before);
     }
   } else {
     for (int e = threadIdx.x; e < E; e += SORT_THREADS) base[e] = 0;
@@ -125,22 +126,20 @@ __global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const ID* __
     __syncthreads();
   }
   if (counts != nullptr) {
-#pragma unroll
-    for (int i = 0; i < MAX_EXPERTS / SORT_THREADS; ++i) {
-      const int e = threadIdx.x + i * SORT_THREADS;
-      if (e < E) base[e] += before[i];
-    }
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) base[e] += whist[e];
     __syncthreads();
   }
 
-  for (int64_t tile = begin; tile < end; tile += SORT_TILE) {
+  const int iters = static_cast<int>(min((per_block + SORT_THREADS - 1) / SORT_THREADS, static_cast<int64_t>(SORT_ITERS)));
+  for (int64_t tile = begin; tile < end; tile += iters * SORT_THREADS) {
     for (int i = threadIdx.x; i < SORT_WARPS * E; i += SORT_THREADS) whist[i] = 0;
     __syncthreads();
     int* mine = whist + warp * E;
     int ranks[SORT_ITERS], picks[SORT_ITERS];
-    const int64_t s0 = tile + warp * 32 * SORT_ITERS + lane;
+    const int64_t s0 = tile + warp * 32 * iters + lane;
 #pragma unroll
     for (int i = 0; i < SORT_ITERS; ++i) {
+      if (i >= iters) break;
       const int64_t s = s0 + i * 32;
       const int e = expert_of(ids, s, end, E);
       const unsigned same = __match_any_sync(0xffffffffu, e);
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const ID* __
 #pragma unroll
     for (int i = 0; i < SORT_ITERS; ++i) {
       const int64_t s = s0 + i * 32;
-      if (s < end) {
+      if (i < iters && s < end) {
         const int row = picks[i] >= 0 ? mine[picks[i]] + ranks[i] : -1;
         pos[s] = row;
         if (row >= 0) order[row] = static_cast<int>(s);
@@ -195,12 +194,13 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// The expert whose rows hold `row`: the last e with offsets[e] <= row.
-__device__ __forceinline__ int expert_of_row(const int* __restrict__ offsets, int E, int row) {
+// The expert whose rows hold `row`: the last e with first[e] <= row; `first` in shared memory, where a step of the search
+// takes a tenth of its time in L2.
+__device__ __forceinline__ int expert_of_row(const int* first, int E, int row) {
   int lo = 0, hi = E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (offsets[mid] <= row) lo = mid;
+    if (first[mid] <= row) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -236,39 +236,40 @@ __global__ void __launch_bounds__(ROW_THREADS) expert_gather_kernel(const uint16
   }
 }
 
-// bf16(RN32(x / s)) with r = RN32(1 / s): x r is within three units of the last place of RN32(x / s) while both are normal numbers, so
-// its rounding to bf16 is the same unless it lies that near the middle between two bf16 numbers (`near`, then the
-// division decides; 1 of 7000).
-__device__ __forceinline__ float quotient_fast(float x, float r, bool& near) {
-  const float q = __fmul_rn(x, r);
-  const uint32_t bits = __float_as_uint(q);
-  const uint32_t exponent = (bits >> 23) & 0xFFu;
-  near |= (bits & 0xFFFFu) - 0x7FFCu <= 8u || (exponent - 2u > 250u && x != 0.0f);
-  return q;
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-// Xs[r] = X[order[r] / top_k] / scales[expert of r]: a block takes a run of sorted rows, most of them of one expert, and 1024
-// columns, so a thread reads its 8 scales and their reciprocals once per expert and not once per row (the scales of a row
+// Xs[r] = bf16(RN32(X[order[r] / top_k] / s)), s the scale of r's expert: a block takes a run of sorted rows, most of them of
+// one expert, and 1024 columns, so a thread reads its 8 scales once per expert and not once per row (the scales of a row
 // are twice its bytes).
-constexpr int RUN = 16;
+// Division-free but for 1 of 4000 elements: with r = RN32(1 / s) a normal number, r- = RN32(r (1 - 2^-22)) and r+ =
+// RN32(r (1 + 2^-22)) enclose 1 / s, so RN32(x r-) and RN32(x r+) enclose RN32(x / s) (rounding keeps order), and where both
+// round to the same bf16 that is the result. Where they do not, the division decides. (8 divisions per 16 bytes, or a test of
+// every quotient's low bits, took twice the time that the rows take from HBM.)
+constexpr int RUN = 32;
 __global__ void __launch_bounds__(ROW_THREADS) expert_gather_scaled_kernel(
     const uint16_t* __restrict__ X, int64_t ldx, int64_t T, int64_t K, const int* __restrict__ offsets, int E,
     const int* __restrict__ order, int top_k, const float* __restrict__ scales, uint16_t* __restrict__ Xs, int64_t ldxs,
     int64_t n_rows) {
-  __shared__ int slots[RUN], experts[RUN];
+  __shared__ int slots[RUN], experts[RUN], first[MAX_EXPERTS];
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * RUN;
+  for (int e = threadIdx.x; e < E; e += ROW_THREADS) first[e] = __ldg(offsets + e);
+  int my_slot = -1;
+  if (threadIdx.x < RUN && r0 + threadIdx.x < n_rows) my_slot = __ldg(order + r0 + threadIdx.x);
+  __syncthreads();
   if (threadIdx.x < RUN) {
-    const int64_t r = r0 + threadIdx.x;
-    int slot = r < n_rows ? order[r] : -1;
-    if (slot >= T * top_k) slot = -1;
-    slots[threadIdx.x] = slot;
-    experts[threadIdx.x] = slot >= 0 ? expert_of_row(offsets, E, static_cast<int>(r)) : -1;
+    if (my_slot >= T * top_k) my_slot = -1;
+    slots[threadIdx.x] = my_slot;
+    experts[threadIdx.x] = my_slot >= 0 ? expert_of_row(first, E, static_cast<int>(r0 + threadIdx.x)) : -1;
   }
   __syncthreads();
   const int64_t c = static_cast<int64_t>(blockIdx.y) * ROW_THREADS + threadIdx.x;
   if (c >= K / 8) return;
-  float s[8], rcp[8];
-  bool odd_scales = false;  // a scale whose reciprocal is no normal number: every row by division
+  uint64_t below[4], above[4];  // r- and r+ of two columns each
+  bool divide = false;          // a scale whose reciprocal is no normal number
   int have = -1;
 #pragma unroll 1
   for (int i0 = 0; i0 < RUN; i0 += AT_ONCE) {
@@ -280,29 +281,39 @@ __global__ void __launch_bounds__(ROW_THREADS) expert_gather_scaled_kernel(
     for (int i = 0; i < AT_ONCE; ++i) {
       if (slots[i0 + i] < 0) continue;
       const int e = experts[i0 + i];
+      const float* sc = scales + e * K + c * 8;
       if (e != have) {
         have = e;
-        const float4* sc = reinterpret_cast<const float4*>(scales + e * K + c * 8);
-        const float4 lo = __ldg(sc), hi = __ldg(sc + 1);
-        s[0] = lo.x; s[1] = lo.y; s[2] = lo.z; s[3] = lo.w; s[4] = hi.x; s[5] = hi.y; s[6] = hi.z; s[7] = hi.w;
-        odd_scales = false;
+        divide = false;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          rcp[k] = __fdiv_rn(1.0f, s[k]);
-          const float size = fabsf(rcp[k]);
-          odd_scales |= !(size >= 1.17549435e-38f && size <= 3.0e38f);
+        for (int k = 0; k < 4; ++k) {
+          const float2 two = __ldg(reinterpret_cast<const float2*>(sc) + k);
+          const float ra = __fdiv_rn(1.0f, two.x), rb = __fdiv_rn(1.0f, two.y);
+          divide |= !(fabsf(ra) >= 2.0e-38f && fabsf(ra) <= 3.0e38f && fabsf(rb) >= 2.0e-38f && fabsf(rb) <= 3.0e38f);
+          below[k] = f32x2_pack(__float_as_uint(ra * (1.0f - 0x1p-22f)), __float_as_uint(rb * (1.0f - 0x1p-22f)));
+          above[k] = f32x2_pack(__float_as_uint(ra * (1.0f + 0x1p-22f)), __float_as_uint(rb * (1.0f + 0x1p-22f)));
         }
       }
-      float f[8], q[8];
-      unpack8(v[i], f);
-      bool near = odd_scales;
+      const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t q[4], differ = divide ? 1u : 0u;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = quotient_fast(f[k], rcp[k], near);
-      if (near) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = __fdiv_rn(f[k], s[k]);
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t two = f32x2_pack(x[k] << 16, x[k] & 0xFFFF0000u);
+        q[k] = f32x2_to_bf16x2(f32x2_mul(two, below[k]));
+        differ |= q[k] ^ f32x2_to_bf16x2(f32x2_mul(two, above[k]));
       }
-      *reinterpret_cast<uint4*>(Xs + (r0 + i0 + i) * ldxs + c * 8) = pack8(q);
+      if (differ != 0u) {
+        float f[8];
+        unpack8(v[i], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = __fdiv_rn(f[k], __ldg(sc + k));
+        const uint4 exact = pack8(f);
+        q[0] = exact.x;
+        q[1] = exact.y;
+        q[2] = exact.z;
+        q[3] = exact.w;
+      }
+      *reinterpret_cast<uint4*>(Xs + (r0 + i0 + i) * ldxs + c * 8) = make_uint4(q[0], q[1], q[2], q[3]);
     }
   }
 }
@@ -358,8 +369,9 @@ __global__ void __launch_bounds__(ROW_THREADS) expert_combine_kernel(const uint1
 __global__ void __launch_bounds__(ROW_THREADS) expert_combine_scaled_kernel(
     const uint16_t* __restrict__ Ys, int64_t ldys, int64_t K, const int* __restrict__ pos, int top_k, int64_t n_rows,
     const int* __restrict__ offsets, int E, const float* __restrict__ scales, uint16_t* __restrict__ Y, int64_t ldy) {
-  __shared__ int rows[ROW_THREADS], experts[ROW_THREADS];
+  __shared__ int rows[ROW_THREADS], experts[ROW_THREADS], first[MAX_EXPERTS];
   const int64_t t = blockIdx.x;
+  for (int e = threadIdx.x; e < E; e += ROW_THREADS) first[e] = __ldg(offsets + e);
   const int64_t c = static_cast<int64_t>(blockIdx.y) * ROW_THREADS + threadIdx.x;
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   for (int j0 = 0; j0 < top_k; j0 += ROW_THREADS) {
@@ -369,7 +381,7 @@ __global__ void __launch_bounds__(ROW_THREADS) expert_combine_scaled_kernel(
       const int row = pos[t * top_k + j0 + threadIdx.x];
       const bool real = row >= 0 && row < n_rows;
       rows[threadIdx.x] = real ? row : -1;
-      experts[threadIdx.x] = real ? expert_of_row(offsets, E, row) : -1;
+      experts[threadIdx.x] = real ? expert_of_row(first, E, row) : -1;
     }
     __syncthreads();
     if (c >= K / 8) continue;
