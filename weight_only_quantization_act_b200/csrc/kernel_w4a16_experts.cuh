@@ -70,7 +70,8 @@ constexpr int THREADS = 32 * (FIRST_DQ + DQ_WARPS);
 constexpr int LAUNCH_REGS = 96, EPI_REGS = 152, OTHER_REGS = 56;
 static_assert(32 * (EPI_WARPS * EPI_REGS + (THREADS / 32 - EPI_WARPS) * OTHER_REGS) <= THREADS * LAUNCH_REGS,
               "the shares fit what the block was launched with");
-constexpr int CHUNKS = BN / 16 / 2;               // blocks of 16 tokens per scaling warp
+constexpr int BLOCK = 32;                         // tokens per load of a scaling warp
+constexpr int CHUNKS = BN / BLOCK / 2;            // blocks per scaling warp
 constexpr int MAX_EXPERTS = 1024;
 constexpr int TABLE_BYTES = 2 * (MAX_EXPERTS + 1) * 4;
 constexpr int SMEM_BYTES = STAGES * X_BYTES + CSTAGES * CSTAGE_BYTES + TABLE_BYTES + 1024;
@@ -468,13 +469,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
       const Tile tile = tile_at(t);
-      const int chunks = static_cast<int>(tile.n() / 16);
-      const int mine = (chunks - half + 1) / 2;  // this warp's blocks: half, half + 2, ...
-      uint64_t y[CHUNKS][8];
+      const int blocks = (tile.tokens + BLOCK - 1) / BLOCK;
+      const int mine = (blocks - half + 1) / 2;  // this warp's blocks: half, half + 2, ...
+      uint64_t y[CHUNKS][BLOCK / 2];
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[c][k] = 0ull;
+        for (int k = 0; k < BLOCK / 2; ++k) y[c][k] = 0ull;
       float2 steps = make_float2(0.0f, 0.0f);
       for (int g = 0; g < num_groups; ++g, ++i) {
         if ((g & 1) == 0) {
@@ -492,16 +493,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         wait(done_bar(i), parity(i), p, kSiteEpiAccFull);
         __syncwarp();
         tc_fence_after();
-        const uint32_t ta = tmem_base + (i & 1u) * BN + static_cast<uint32_t>(half * 16) + (static_cast<uint32_t>(quarter * 32) << 16);
-        uint32_t v[2][16];
-        if (mine > 0) dq::tmem_ld16_issue(ta, v[0]);
+        const uint32_t ta = tmem_base + (i & 1u) * BN + static_cast<uint32_t>(half * BLOCK) + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
           if (c >= mine) break;
-          dq::tmem_wait_ld16(v[c & 1]);
-          if (c + 1 < mine) dq::tmem_ld16_issue(ta + static_cast<uint32_t>((c + 1) * 32), v[(c + 1) & 1]);
+          float v[BLOCK];  // columns past the tile's are of no token
+          tmem_ld32(ta + static_cast<uint32_t>(c * 2 * BLOCK), v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) fma_f32x2(y[c][k], ss, v[c & 1][2 * k], v[c & 1][2 * k + 1]);
+          for (int k = 0; k < BLOCK / 2; ++k) fma_f32x2(y[c][k], ss, __float_as_uint(v[2 * k]), __float_as_uint(v[2 * k + 1]));
         }
         tc_fence_before();
         __syncwarp();
@@ -522,9 +521,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c) {
         if (c >= mine) break;
-        const int tok0 = (2 * c + half) * 16;
+        const int tok0 = (2 * c + half) * BLOCK;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < BLOCK / 2; ++k) {
           uint32_t lo, hi;
           asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(y[c][k]));
           if (GATED) {
