@@ -355,7 +355,7 @@ AWQ_API awq_status awq_expert_combine_backward(const void *dY, int64_t T, int64_
  * Products of the experts (W4A16): Y[r] = Xs[r] deq(W_e)^T for the rows offsets[e] <= r < offsets[e + 1] of
  * every expert e, or with gated = 1 the gated form of awq_w4a16_gemv. The weights enter with
  * their exact value, (q - z) summed per group and scaled by the fp32 step; only in a group with |z| > 240 (its
- * weights nearly equal) an expert with more than 16 rows takes q - z rounded to bf16.
+ * weights nearly equal) an expert with more than 8 rows takes q - z rounded to bf16.
  *   Xs      device bf16 [R, K] sorted rows, row stride ldx (multiple of 8)
  *   codes   device uint32 [E, O, K/8], 16-byte aligned; steps / zeros device float [E, O, K/128]
  *   Y       device bf16 [R, O] (gated: [R, O/2]), row stride ldy >= its columns; rows from offsets[E] on are left

@@ -273,7 +273,7 @@ extern "C" awq_status awq_expert_combine_backward(const void* dY, int64_t T, int
 
 // --------------------------------------------------------------------------------------- experts' products
 namespace {
-constexpr int kFewRows = 16;  // experts with up to this many rows run the few-token kernel
+constexpr int kFewRows = 8;  // experts with up to this many rows run the few-token kernel
 }
 
 extern "C" size_t awq_w4a16_experts_workspace_size(int64_t R, int64_t E, int64_t K, int64_t O) {

@@ -21,12 +21,18 @@
 // A CTA of 4 warps owns 128 weight rows (gated: 64 gate rows and the 64 up rows of the same outputs) and a
 // slice of the groups; a warp owns 32 rows, two MMA tiles, so a piece of X read from shared memory serves both. A
 // lane loads the 16-byte pieces that it will itself unpack (rows l / 4 + 0, 8, 16, 24, 32 codes of a group each)
-// straight into registers, a group ahead, out of L2, where each thread has called one row's next groups with a bulk
-// prefetch. X as fp16, its sums (MMAs too, with a constant operand), the steps and the zero points of a chunk of groups
-// stand in shared memory. Both MMA operands name the in-features of a group in the order that the unpacking gives,
+// straight into registers, three groups ahead, the L2 fetching a row's next three groups along. X as fp16, its sums
+// (MMAs too, with a constant operand), the steps and the zero points of a chunk of groups stand in shared
+// memory. Both MMA operands name the in-features of a group in the order that the unpacking gives,
 // so X is permuted once, on its way there. The slices of a row block are the CTAs of one cluster (at most 8), which
 // add their fp32 partial sums through distributed shared memory in slice order: one launch, no workspace, the same
 // result every time.
+//
+// Measured (B200, one call after another, weights of one token and of 8 experts with 2 rows each): 28672 -> 8192 in 34 us and
+// 8 x (4096 -> 2 x 14336) in 145 us, 3.9 and 3.6 TB/s of packed weights. What bounds it is how many loads the SM keeps in
+// flight and how they fall on DRAM pages: with one group ahead and 4 CTAs per SM 36 and 201 us, with three ahead and 4 CTAs
+// (which spills, and opens more rows at once) 36 and 235, with seven ahead and 2 CTAs 35 and 163; with a bulk prefetch of
+// each row into L2 instead 36 and 201; without the loads, the rest takes 25 and 108.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -41,9 +47,8 @@ constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int ROWS = 32 * WARPS;                       // weight rows per CTA
 constexpr int TOKENS = 8;                              // tokens per pass over the weights
-constexpr int DEPTH = 2;                               // groups in registers: one in use, one on its way
-constexpr int AHEAD = 32;                              // groups called into L2 ahead
-constexpr int CTAS_PER_SM = 4;
+constexpr int DEPTH = 4;                               // groups in registers: one in use, three on their way
+constexpr int CTAS_PER_SM = 3;
 constexpr int PART_LD = ROWS + 4;                      // partial sums [TOKENS][PART_LD]
 constexpr int PART_BYTES = TOKENS * PART_LD * 4;
 constexpr int PARAM_LD = ROWS + 1;                     // steps and zero points [group][PARAM_LD], written down a column
@@ -83,10 +88,6 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// Calls `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -103,10 +104,10 @@ __device__ __forceinline__ float2 lds64f(uint32_t a) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
   return v;
 }
-// Weights are read once: not kept in L1.
+// 16 bytes of codes; the L2 fetches the 256 bytes around them, four groups of the row.
 __device__ __forceinline__ uint4 ldg_codes(const uint32_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -189,11 +190,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
   const uint32_t* code[4];  // the lane's pieces of its rows g8, g8 + 8, g8 + 16, g8 + 24
 #pragma unroll
   for (int j = 0; j < 4; ++j) code[j] = codes + weight_row(g8 + 8 * j) * (p.K / 8) + t4 * 4;
-  const uint32_t* my_codes = codes + weight_row(lane) * (p.K / 8);  // the row that this thread calls into L2
-  auto call = [&](int g, int n) {  // groups g..g+n-1 of the slice
-    if (g < n_groups) prefetch_l2(my_codes + g * 16, static_cast<uint32_t>(min(n, n_groups - g) * 64));
-  };
-
   uint4 w[DEPTH][4];
   auto load = [&](int d, int g) {
     if (g < n_groups) {
@@ -279,7 +275,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
     }
   };
 
-  call(0, AHEAD);
   for (int64_t m0 = 0; m0 < rows; m0 += TOKENS) {
     const int mt = static_cast<int>(min(rows - m0, static_cast<int64_t>(TOKENS)));
     float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
@@ -321,7 +316,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
       const float* ba = back + 2 * t4;
       uint32_t xa = x_lane;
       for (int g0 = 0; g0 < chunk; g0 += DEPTH) {
-        call(chunk0 + g0 + AHEAD, DEPTH);
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
           if (g0 + d >= chunk) break;
