@@ -20,7 +20,9 @@
 //
 // Bounds: at N = 192 a group takes the tensor cores 768 cycles, the unpacking about 200 and the scaling about 140
 // issue cycles of every SM quarter. Below N = 60 the codes arrive no faster than that from HBM (9 KB per SM and
-// group). 192 and not 256 tokens: two accumulators of N columns and four operand buffers of 32 fill tensor memory.
+// group). 192 and not 256 tokens: two accumulators of N columns and two operand buffers of 64 fill tensor memory. Where
+// every tile of the call is narrower, three groups (up to 96 tokens) or four (up to 64) are in flight instead of two: the
+// way from a group's end through the unpackers and scaling warps to the next group's MMAs takes about 2000 cycles.
 //
 // Persistent, clusters of 2 CTAs, one CTA per SM; every CTA makes the table of tiles from the row offsets for
 // itself and takes each n-th tile, so nothing is exchanged between pairs. Warps of a CTA:
@@ -76,8 +78,9 @@ constexpr int MAX_EXPERTS = 1024;
 constexpr int TABLE_BYTES = 2 * (MAX_EXPERTS + 1) * 4;
 constexpr int SMEM_BYTES = STAGES * X_BYTES + CSTAGES * CSTAGE_BYTES + TABLE_BYTES + 1024;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t A_COL0 = 2 * BN;
-static_assert(A_COL0 + 2 * A_COLS <= TMEM_COLS, "accumulators and operand buffers fit tensor memory");
+static_assert(2 * (BN + A_COLS) <= TMEM_COLS && 3 * (96 + A_COLS) <= TMEM_COLS && 4 * (64 + A_COLS) <= TMEM_COLS &&
+                  STAGES >= 4,
+              "accumulators and operand buffers fit tensor memory");
 static_assert(SMEM_BYTES <= 232448, "fits the 227 KB of dynamic shared memory");
 static_assert(X_HALF_BYTES % 1024 == 0 && CSTAGE_BYTES % 1024 == 0 && BN / 2 == 3 * X_BOX,
               "tiles stay 1024-byte aligned and the largest box fits");
@@ -209,6 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t bars[2 * STAGES + 2 * CSTAGES + 1];
   __shared__ uint32_t tmem_slot;
+  __shared__ int widest;  // tokens of the call's widest tile
   int* first_row = reinterpret_cast<int*>(smem + STAGES * X_BYTES + CSTAGES * CSTAGE_BYTES);  // [E + 1]
   int* first_tile = first_row + MAX_EXPERTS + 1;                                              // [E + 1]
 
@@ -216,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t bar0 = smem_u32(&bars[0]);
-  // group i of this pair's tiles, numbered through them: stage i % 4, phase i / 4; accumulator and operand i % 2
+  // group i of this pair's tiles, numbered through them: stage i % 4, phase i / 4; accumulator and operand i % depth
   auto full_bar = [&](uint32_t i) { return bar0 + 8u * (i % STAGES); };             // even CTA: group can be issued
   auto done_bar = [&](uint32_t i) { return bar0 + 8u * (STAGES + i % STAGES); };    // group accumulated
   auto parity = [](uint32_t i) { return (i / STAGES) & 1u; };
@@ -252,11 +256,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     first_row[e] = min(max(p.offsets[e], 0), static_cast<int>(p.R));
   __syncthreads();
   if (warp == 2) {
-    int carry = 0;
+    int carry = 0, most = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       const int rows = e < p.E ? max(first_row[e + 1] - first_row[e], 0) : 0;
       const int tiles = rows >= p.min_rows ? token_tiles(rows) * p.n_bands : 0;
+      if (tiles > 0) most = max(most, min(rows, tile_rows(rows, token_tiles(rows))));
       int inc = tiles;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -266,7 +271,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (e < p.E) first_tile[e] = carry + inc - tiles;
       carry += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) first_tile[p.E] = carry;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      first_tile[p.E] = carry;
+      widest = most;
+    }
   }
   tc_fence_before();
   cluster_sync();
@@ -278,6 +287,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int num_tiles = first_tile[p.E];
   const int num_groups = static_cast<int>(p.G);
   const int num_slots = (num_groups + 1) / 2;
+  // groups in flight, and the columns of each: an accumulator, then an operand buffer
+  const uint32_t depth = widest > 96 ? 2u : widest > 64 ? 3u : 4u;
+  const uint32_t acc_cols = widest > 96 ? BN : widest > 64 ? 96u : 64u, buf_cols = acc_cols + A_COLS;
   auto tile_at = [&](int t) { return tile_of(t, first_tile, first_row, p.E); };
 
   if (warp < FIRST_EPI) {
@@ -303,15 +315,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     } else if (warp == 1 && rank == 0 && elect_one()) {
       // ------------------------------------------------------------------------------ MMA (even CTA)
-      uint32_t i = 0;
+      uint32_t i = 0, buf = 0;
       const uint64_t desc0 = smem_desc_sw128(x_tile(0));
       for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
         const uint32_t idesc = idesc_bf16_f32(2 * HALF, tile_at(t).n());
         for (int g = 0; g < num_groups; ++g, ++i) {
           wait(full_bar(i), parity(i), p, kSiteMmaFull);
           tc_fence_after();
-          const uint32_t d = tmem_base + (i & 1u) * BN;
-          const uint32_t a = tmem_base + A_COL0 + (i & 1u) * A_COLS;
+          const uint32_t d = tmem_base + buf * buf_cols, a = d + acc_cols;
+          if (++buf == depth) buf = 0;
           const uint64_t b = desc0 + (i % STAGES) * (X_BYTES >> 4);
 #pragma unroll
           for (int kk = 0; kk < 2 * BK / UK; ++kk)  // 16 in-features: 8 columns of A, 32 bytes of B's rows
@@ -410,8 +422,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3;
     const int r = lane + 32 * quarter;      // the lane's row of the CTA's 128
     const uint32_t sw = static_cast<uint32_t>(r & 7);
+    const uint32_t ta = tmem_base + acc_cols + static_cast<uint32_t>(set * (BK / 2)) + (static_cast<uint32_t>(quarter * 32) << 16);
     int slot = 0;
-    uint32_t phase = 0, i = 0;
+    uint32_t phase = 0, i = 0, buf = 0;
     for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
       for (int g = 0; g < num_groups; ++g, ++i) {
         const int odd = g & 1;  // a slot's second group
@@ -444,12 +457,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             phase ^= 1u;
           }
         }
-        if (i >= 2) wait(done_bar(i - 2), parity(i - 2), p, kSiteTmaProduced);
+        if (i >= depth) wait(done_bar(i - depth), parity(i - depth), p, kSiteTmaProduced);
         __syncwarp();
         tc_fence_after();  // the MMAs that read the buffer come before the stores below
-        tmem_st32(tmem_base + A_COL0 + (i & 1u) * A_COLS + static_cast<uint32_t>(set * (BK / 2)) +
-                      (static_cast<uint32_t>(quarter * 32) << 16),
-                  o);
+        tmem_st32(ta + buf * buf_cols, o);
+        if (++buf == depth) buf = 0;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -462,11 +474,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, half = (warp - FIRST_EPI) / 4;
     const int r = lane + 32 * quarter;
     int slot = 0;
-    uint32_t phase = 0, i = 0;
-    if (lane == 0) {  // both accumulators are free
-      mbar_arrive_pair(map_to_rank(full_bar(0), 0));
-      mbar_arrive_pair(map_to_rank(full_bar(1), 0));
-    }
+    uint32_t phase = 0, i = 0, buf = 0;
+    if (lane == 0)  // every accumulator is free
+      for (uint32_t d = 0; d < depth; ++d) mbar_arrive_pair(map_to_rank(full_bar(d), 0));
     for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
       const Tile tile = tile_at(t);
       const int blocks = (tile.tokens + BLOCK - 1) / BLOCK;
@@ -493,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         wait(done_bar(i), parity(i), p, kSiteEpiAccFull);
         __syncwarp();
         tc_fence_after();
-        const uint32_t ta = tmem_base + (i & 1u) * BN + static_cast<uint32_t>(half * BLOCK) + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t ta = tmem_base + buf * buf_cols + static_cast<uint32_t>(half * BLOCK) + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
           if (c >= mine) break;
@@ -504,7 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(map_to_rank(full_bar(i + 2), 0));  // the group that overwrites it
+        if (lane == 0) mbar_arrive_pair(map_to_rank(full_bar(i + depth), 0));  // the group that overwrites it
+        if (++buf == depth) buf = 0;
       }
       if (status_code(st) != 0u) break;  // nothing of an unfinished tile is stored
 
