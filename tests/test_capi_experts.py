@@ -81,6 +81,10 @@ def test_experts_refusals(lib):
     assert call(codes=ODD) == 1 and call(zeros=ODD) == 1 and call(O=0) == 1 and call(O=63, gated=1) == 1
     assert call(Y=None) == 1 and call(ldy=63) == 1 and call(gated=3) == 1
     assert call(ws=None) == 3 and call(wsb=8) == 3 and call(ws=ODD) == 1
+    # refused before anything is launched, whichever of the two kernels would refuse it
+    assert call(R=9, E=1024, O=1 << 21, ldy=1 << 21) == 1 and "too many" in lib.awq_last_error().decode()
+    assert call(R=(1 << 31) - 1, E=1024, O=1 << 20, ldy=1 << 20) == 1 and "too many" in lib.awq_last_error().decode()
+    assert call(O=1 << 24, ldy=1 << 24) == 1 and "too large" in lib.awq_last_error().decode()
     assert lib.awq_w4a16_experts_workspace_size(4, 8, 256, 64) >= 16
     assert lib.awq_w4a16_experts_workspace_size(4, 0, 256, 64) == 0
 
@@ -94,3 +98,42 @@ def test_binding_refusals():
                  lambda: awq.expert_gather_backward(cpu, None), lambda: awq.expert_combine_backward(cpu, cpu, None, steps)):
         with pytest.raises(TypeError):
             call()
+
+
+class _Elsewhere(torch.Tensor):
+    """A tensor that says it lives on a CUDA device."""
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", 5))
+
+    def get_device(self):
+        return 5
+
+
+def test_device_of_arguments_given_by_name(monkeypatch):
+    seen = []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            seen.append(self.device)
+
+        def __exit__(self, *_):
+            return False
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    ids = torch.zeros(2, 2, dtype=torch.int64).as_subclass(_Elsewhere)
+    call = awq._on_stream(lambda ids, n_experts: n_experts)
+    for run in (lambda: call(ids, 4), lambda: call(ids, n_experts=4), lambda: call(n_experts=4, ids=ids)):
+        seen.clear()
+        assert run() == 4 and seen == [torch.device("cuda", 5)]
+
+
+def test_workspace_refusals():
+    cpu = torch.device("cpu")
+    awq._on_device("workspace", torch.zeros(4), cpu)
+    for bad in (torch.zeros(4, 4).t(), torch.zeros(4, device="meta"), [0], None):
+        with pytest.raises(ValueError):
+            awq._on_device("workspace", bad, cpu)

@@ -448,8 +448,10 @@ def _on_stream(fn):
 
     @functools.wraps(fn)
     def wrapper(*args, stream=None, **kwargs):
-        first = args[0] if args else next(iter(kwargs.values()))
-        on_cuda = isinstance(first, torch.Tensor) and first.is_cuda
+        first = args[0] if args else None
+        if not isinstance(first, torch.Tensor):  # arguments given by name, in any order
+            first = next((t for t in (*args, *kwargs.values()) if isinstance(t, torch.Tensor)), None)
+        on_cuda = first is not None and first.is_cuda
         if stream is not None:
             if on_cuda and stream.device != first.device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
@@ -490,6 +492,12 @@ def _tensor(name: str, t: torch.Tensor, dtype, shape, device) -> int:
     if t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be contiguous, of shape {list(shape)} and on {device}")
     return t.data_ptr()
+
+
+def _on_device(name: str, t: torch.Tensor, device) -> None:
+    """A caller's workspace: its bytes from its first element on are the library's."""
+    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
 
 
 def _rows_out(name: str, out: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
@@ -566,6 +574,8 @@ def expert_sort(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor | Non
     pos = ids.new_empty(ids.shape, dtype=torch.int32)
     need = lib.awq_expert_sort_workspace_size(n, n_experts)
     ws = _workspace(need, ids.device, workspace) if need else None
+    if need:
+        _on_device("workspace", ws, ids.device)
     _check("awq_expert_sort", lib.awq_expert_sort(
         ids.data_ptr(), ids.element_size(), n, n_experts, ws.data_ptr() if need else None, need, offsets.data_ptr(),
         order.data_ptr(), pos.data_ptr(), _current_stream()))
@@ -668,12 +678,13 @@ def w4a16_experts(Xs: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor, 
     lib = load_library()
     Xs = _rows("Xs", Xs)
     R, K = Xs.shape
-    E = codes.shape[0]
+    E = codes.shape[0] if isinstance(codes, torch.Tensor) and codes.dim() == 3 else 0  # _packed refuses the others
     O, c, s, z = _packed(codes, steps, zeros, (E,), K, Xs.device)
     first = _tensor("offsets", offsets, torch.int32, (E + 1,), Xs.device)
     out = _rows_out("out", out, R, O // 2 if gated else O, Xs)
     if workspace is None:
         workspace = w4a16_experts_workspace(codes, R)
+    _on_device("workspace", workspace, Xs.device)
     _check("awq_w4a16_experts", lib.awq_w4a16_experts(
         Xs.data_ptr(), R, K, _ld(Xs), first, E, c, s, z, O, bool(gated), out.data_ptr(), out.stride(0), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _current_stream()))

@@ -33,13 +33,22 @@ awq_status check_experts(int64_t E) {
   return AWQ_OK;
 }
 
+int64_t few_row_blocks(int64_t O, bool gated) {
+  const int64_t out_rows = gated ? awq::few::ROWS / 2 : awq::few::ROWS;
+  return ((gated ? O / 2 : O) + out_rows - 1) / out_rows;
+}
+
+awq_status check_few_rows(int64_t O, bool gated) {
+  if (few_row_blocks(O, gated) > 65535)  // the grid's y extent
+    return fail(AWQ_ERR_INVALID_ARG, "O (%lld) is too large", static_cast<long long>(O));
+  return AWQ_OK;
+}
+
 // Rows of every expert, or of the one layer (E = 1, offsets null), through the few-token kernel. `active` experts
 // can have rows, each up to `tokens` of them.
 awq_status launch_few(awq::few::Params& p, int64_t E, int64_t active, int64_t tokens, bool gated, int sms,
                       cudaStream_t st) {
-  const int64_t out_rows = gated ? awq::few::ROWS / 2 : awq::few::ROWS;
-  const int64_t n_rb = ((gated ? p.O / 2 : p.O) + out_rows - 1) / out_rows;
-  if (n_rb > 65535) return fail(AWQ_ERR_INVALID_ARG, "O (%lld) is too large", static_cast<long long>(p.O));
+  const int64_t n_rb = few_row_blocks(p.O, gated);
   // The number of slices that takes the fewest steps: waves of CTAs times a CTA's groups, and what a CTA does before
   // and after them, which takes about as long as 10 groups.
   int64_t slices = 1, best = 0;
@@ -87,6 +96,7 @@ extern "C" awq_status awq_w4a16_gemv(const void* X, int64_t M, int64_t K, int64_
   AWQ_TRY(check_output("Y", Y, M, gated ? O / 2 : O, ldy));
   if (bias != nullptr && gated) return fail(AWQ_ERR_INVALID_ARG, "bias and gated cannot be combined");
   if ((reinterpret_cast<uintptr_t>(bias) & 1u) != 0) return fail(AWQ_ERR_INVALID_ARG, "bias is not 2-byte aligned");
+  AWQ_TRY(check_few_rows(O, gated != 0));
   DeviceInfo* d = nullptr;
   AWQ_TRY(device_info(&d));
   awq::few::Params p = {};
@@ -102,7 +112,6 @@ extern "C" awq_status awq_w4a16_gemv(const void* X, int64_t M, int64_t K, int64_
   p.O = O;
   p.K = K;
   p.G = K / 128;
-  p.max_rows = AWQ_GEMV_MAX_TOKENS;
   AWQ_TRY(launch_few(p, 1, 1, M, gated != 0, d->sms, reinterpret_cast<cudaStream_t>(stream)));
   return ok();
 }
@@ -272,10 +281,6 @@ extern "C" awq_status awq_expert_combine_backward(const void* dY, int64_t T, int
 }
 
 // --------------------------------------------------------------------------------------- experts' products
-namespace {
-constexpr int kFewRows = 8;  // experts with up to this many rows run the few-token kernel
-}
-
 extern "C" size_t awq_w4a16_experts_workspace_size(int64_t R, int64_t E, int64_t K, int64_t O) {
   if (R < 1 || E < 1 || E > AWQ_MAX_EXPERTS || K < 128 || O < 1) return 0;
   return 512;  // status word
@@ -293,8 +298,21 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   if (workspace == nullptr || ws_bytes < need)
     return fail(AWQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? ws_bytes : 0);
   if (!aligned16(workspace)) return fail(AWQ_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  // Experts of up to 8 rows run the few-token kernel, the others the grouped one. Everything that can be refused is
+  // looked at before the first of the two is launched.
+  const bool grouped = R > awq::few::TOKENS;
+  const int64_t tile_out = gated ? awq::grp::HALF : 2 * awq::grp::HALF;
+  const int64_t n_bands = ((gated ? O / 2 : O) + tile_out - 1) / tile_out;
+  AWQ_TRY(check_few_rows(O, gated));
+  if (grouped && (E * O >= (1ll << 31) || (R / awq::grp::BN + E) * n_bands >= (1ll << 31)))
+    return fail(AWQ_ERR_INVALID_ARG, "too many weight rows or tiles");
   DeviceInfo* d = nullptr;
   AWQ_TRY(device_info(&d));
+  CUtensorMap tmX[3], tmC;  // boxes of 32, 64 and 96 rows
+  if (grouped) {
+    for (int i = 0; i < 3; ++i) AWQ_TRY(make_tmap(&tmX[i], Xs, R, K, ldx, (i + 1) * awq::grp::X_BOX));
+    AWQ_TRY(make_tmap_codes_sw128(&tmC, codes, E * O, K / 8, gated ? 16 : awq::grp::HALF));
+  }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   awq::few::Params p = {};
   p.X = static_cast<const uint16_t*>(Xs);
@@ -309,17 +327,8 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   p.O = O;
   p.K = K;
   p.G = K / 128;
-  p.max_rows = kFewRows;
   AWQ_TRY(launch_few(p, E, std::min(E, R), R, gated != 0, d->sms, st));
-  if (R <= kFewRows) return ok();
-
-  const int64_t tile_out = gated ? awq::grp::HALF : 2 * awq::grp::HALF;
-  const int64_t n_bands = ((gated ? O / 2 : O) + tile_out - 1) / tile_out;
-  if (E * O >= (1ll << 31) || (R / awq::grp::BN + E) * n_bands >= (1ll << 31))
-    return fail(AWQ_ERR_INVALID_ARG, "too many weight rows or tiles");
-  CUtensorMap tmX[3], tmC;  // boxes of 32, 64 and 96 rows
-  for (int i = 0; i < 3; ++i) AWQ_TRY(make_tmap(&tmX[i], Xs, R, K, ldx, (i + 1) * awq::grp::X_BOX));
-  AWQ_TRY(make_tmap_codes_sw128(&tmC, codes, E * O, K / 8, gated ? 16 : awq::grp::HALF));
+  if (!grouped) return ok();
   awq::grp::Params q = {};
   q.offsets = offsets;
   q.steps = steps;
@@ -330,7 +339,6 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   q.G = K / 128;
   q.ldy = ldy;
   q.E = static_cast<int>(E);
-  q.min_rows = kFewRows + 1;
   q.n_bands = static_cast<int>(n_bands);
   q.pair_params = q.G % 2 == 0 && ((reinterpret_cast<uintptr_t>(steps) | reinterpret_cast<uintptr_t>(zeros)) & 7u) == 0;
   q.status = static_cast<awq::DeviceStatus*>(workspace);

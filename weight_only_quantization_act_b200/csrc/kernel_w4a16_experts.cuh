@@ -1,6 +1,6 @@
 // kernel_w4a16_experts.cuh - products of many rows with their experts' packed 4-bit weights: Y[r] = X'[r] deq(W_e)^T
 // for the sorted rows of each expert, optionally with the SiLU gate of a stacked gate and up projection in the
-// epilogue. An expert with few rows is left to kernel_w4a16_few.cuh.
+// epilogue. An expert with up to 8 rows is left to kernel_w4a16_few.cuh.
 //
 // Mathematics: Y[m, o] = sum_g step[o, g] sum_{k in g} (q[o, k] - z[o, g]) x'[m, k]. The tensor cores sum a group's
 // q - z, exact in bf16, into a fresh fp32 accumulator; the epilogue warps scale each group by its fp32 step and add
@@ -29,12 +29,12 @@
 //   0      TMA of this CTA's half of the tile's token rows, a group at a time (two boxes of 64 in-features, 128-byte
 //          swizzle, the box's height 32, 64 or 96 rows), into a ring of 4
 //   1      tensor memory; the even CTA issues the pair MMAs (cta_group::2, M = 256, N, K = 16, A from tensor memory)
-//          into two accumulators in turn, one group each
+//          into two to four accumulators in turn, one group each
 //   2      TMA of the code words, 128 rows x 256 in-features at a time (128 bytes of a row), into a ring of its own
 //   3      steps and zero points of those rows and groups by cp.async, counted on the same barrier
-//   4-11   scaling and epilogue: two warps per quarter of the rows, alternate blocks of 16 tokens
-//   12-19  unpackers: two sets of four warps, one for each half of a group, a weight row per lane, into two operand
-//          buffers
+//   4-11   scaling and epilogue: two warps per quarter of the rows, alternate blocks of 32 tokens
+//   12-19  unpackers: two sets of four warps, one for each half of a group, a weight row per lane, into as many
+//          operand buffers
 // The thread that issues the MMAs waits once per group: one barrier counts the token rows, the unpacked operand and the
 // reading of the accumulator that the group will overwrite, and one commit per group tells all three that it is done
 // (with a wait and a commit for each, and per 64 in-features, that thread took 1700 cycles per group). Every wait
@@ -92,7 +92,6 @@ struct Params {
   uint16_t* Y;             // [R][ldy]
   int64_t R, O, G, ldy;
   int E;
-  int min_rows;            // experts with fewer rows are left to another kernel
   int n_bands;             // tiles along the weight rows
   int pair_params;         // steps and zero points of two groups can be copied as 8 bytes
   DeviceStatus* status;
@@ -148,14 +147,6 @@ __device__ __forceinline__ void umma_bf16_pair_ts(uint32_t d_tmem, uint32_t a_tm
 // k-block).
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-      "%14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 // y += s * v on both fp32 lanes, v given as two registers.
 __device__ __forceinline__ void fma_f32x2(uint64_t& y, uint64_t s, uint32_t lo, uint32_t hi) {
@@ -251,16 +242,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tmX3);
     tma_prefetch_desc(&tmC);
   }
-  // the table of tiles, with the rows clamped so that whatever stands in offsets no access leaves X and Y
+  // the table of tiles, with the rows clamped and rising, so that whatever stands in offsets no access leaves X and Y and
+  // the tiles are as few as the host has counted
   for (int e = static_cast<int>(threadIdx.x); e <= p.E; e += THREADS)
     first_row[e] = min(max(p.offsets[e], 0), static_cast<int>(p.R));
   __syncthreads();
   if (warp == 2) {
     int carry = 0, most = 0;
+    for (int e0 = 0; e0 <= p.E; e0 += 32) {  // running maximum
+      const int e = e0 + lane;
+      int row = e <= p.E ? first_row[e] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, row, d);
+        if (lane >= d) row = max(row, o);
+      }
+      row = max(row, carry);
+      if (e <= p.E) first_row[e] = row;
+      carry = __shfl_sync(0xffffffffu, row, 31);
+    }
+    __syncwarp();
+    carry = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      const int rows = e < p.E ? max(first_row[e + 1] - first_row[e], 0) : 0;
-      const int tiles = rows >= p.min_rows ? token_tiles(rows) * p.n_bands : 0;
+      const int rows = e < p.E ? first_row[e + 1] - first_row[e] : 0;
+      const int tiles = rows > few::TOKENS ? token_tiles(rows) * p.n_bands : 0;
       if (tiles > 0) most = max(most, min(rows, tile_rows(rows, token_tiles(rows))));
       int inc = tiles;
 #pragma unroll

@@ -46,7 +46,7 @@ namespace few {
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int ROWS = 32 * WARPS;                       // weight rows per CTA
-constexpr int TOKENS = 8;                              // tokens per pass over the weights
+constexpr int TOKENS = 8;                              // tokens at most, of the layer or of an expert
 constexpr int DEPTH = 4;                               // groups in registers: one in use, three on their way
 constexpr int CTAS_PER_SM = 3;
 constexpr int PART_LD = ROWS + 4;                      // partial sums [TOKENS][PART_LD]
@@ -55,7 +55,7 @@ constexpr int PARAM_LD = ROWS + 1;                     // steps and zero points 
 constexpr int CHUNK = 32;                              // groups per chunk of X, 16 for 8 tokens: multiples of DEPTH
 constexpr int MAX_SLICES = 8;                          // portable cluster size
 
-// Shared memory for chunks of `xg` groups of `mp` tokens (mp = 1, 2, 4 or 8): 4 CTAs fit an SM.
+// Shared memory for chunks of `xg` groups of `mp` tokens (mp = 1, 2, 4 or 8).
 __host__ __device__ constexpr int smem_bytes(int xg, int mp) {
   return PART_BYTES + xg * 256 * mp + (xg * PARAM_LD + 1) / 2 * 16 + xg * TOKENS * 12;
 }
@@ -73,25 +73,16 @@ struct Params {
   const int* offsets;       // [E + 1] first row of each expert, or null: one layer, rows 0..R-1
   uint16_t* Y;              // [R][ldy] bf16
   int64_t R, ldx, ldy, O, K, G;
-  int max_rows;             // experts with more rows are left to another kernel
   int g_per;                // groups per slice
   int xg;                   // groups per X chunk
   int mp_log2;              // log2 of the tokens that the X chunk has room for
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -164,7 +155,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
     row0 = min(max(static_cast<int64_t>(p.offsets[e]), int64_t(0)), p.R);
     rows = min(max(static_cast<int64_t>(p.offsets[e + 1]), row0), p.R) - row0;
   }
-  if (rows == 0 || rows > p.max_rows) return;  // the same for every CTA of the cluster
+  // the same for every CTA of the cluster; experts with more rows are left to another kernel
+  if (rows == 0 || rows > TOKENS) return;
+  const int mt = static_cast<int>(rows);
 
   const int64_t n_out = GATED ? p.O / 2 : p.O;
   constexpr int OUT_ROWS = GATED ? ROWS / 2 : ROWS;
@@ -198,12 +191,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
     }
   };
 
-  // X of tokens m0..m0+mt-1 and groups gc..gc+ng-1 as fp16, scaled and permuted so that one 16-byte piece (in-features
+  // X of the tokens and of groups gc..gc+ng-1 as fp16, scaled and permuted so that one 16-byte piece (in-features
   // 8w..8w+7) holds the pairs (0, 4), (1, 5), (2, 6), (3, 7). The 16 threads of a token's group are neighbours.
-  auto stage_x = [&](int64_t m0, int mt, int gc, int ng) {
+  auto stage_x = [&](int gc, int ng) {
     const int per_token = ng * 16;
     constexpr int AT_ONCE = 4;  // loads in flight per thread
-    const uint16_t* src = p.X + (row0 + m0) * p.ldx + static_cast<int64_t>(gc) * 128;
+    const uint16_t* src = p.X + row0 * p.ldx + static_cast<int64_t>(gc) * 128;
     int m = 0, c = static_cast<int>(threadIdx.x);  // the thread's next token and 16-byte piece
     while (c >= per_token) c -= per_token, ++m;
     // all threads of a warp take the same number of turns: its pieces are of neighbouring groups, 16 threads each
@@ -275,128 +268,124 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
     }
   };
 
-  for (int64_t m0 = 0; m0 < rows; m0 += TOKENS) {
-    const int mt = static_cast<int>(min(rows - m0, static_cast<int64_t>(TOKENS)));
-    float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+  float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-    for (int d = 0; d < DEPTH - 1; ++d) load(d, d);
-    for (int chunk0 = 0; chunk0 < n_groups; chunk0 += p.xg) {
-      const int chunk = min(p.xg, n_groups - chunk0);
-      __syncthreads();  // the previous chunk has been read
-      if (lane < chunk) {  // steps and zero points, a row of this warp's at a time: a row's groups are neighbours
-        const int64_t first = (e * p.O + weight_row(0)) * p.G + g_begin + chunk0 + lane;
-        const float* ps = p.steps + first;
-        const float* pz = p.zeros + first;
-        const int64_t up = n_out * p.G;                            // gated: from a gate row to its up row
-        int rows_left = static_cast<int>(min(n_out - 1 - weight_row(0), int64_t(32)));  // rows past the end: the last one's
-        uint32_t dst = smem_u32(param + lane * PARAM_LD + warp * 32);
+  for (int d = 0; d < DEPTH - 1; ++d) load(d, d);
+  for (int chunk0 = 0; chunk0 < n_groups; chunk0 += p.xg) {
+    const int chunk = min(p.xg, n_groups - chunk0);
+    __syncthreads();  // the previous chunk has been read
+    if (lane < chunk) {  // steps and zero points, a row of this warp's at a time: a row's groups are neighbours
+      const int64_t first = (e * p.O + weight_row(0)) * p.G + g_begin + chunk0 + lane;
+      const float* ps = p.steps + first;
+      const float* pz = p.zeros + first;
+      const int64_t up = n_out * p.G;                            // gated: from a gate row to its up row
+      int rows_left = static_cast<int>(min(n_out - 1 - weight_row(0), int64_t(32)));  // rows past the end: the last one's
+      uint32_t dst = smem_u32(param + lane * PARAM_LD + warp * 32);
 #pragma unroll 4
-        for (int r = 0; r < (GATED ? 16 : 32); ++r) {
-          // gated: gate row r is row r % 8 of MMA tile r / 8, its up row 8 behind it
-          const uint32_t to = dst + static_cast<uint32_t>((GATED ? (r >> 3) * 16 + (r & 7) : r) * 8);
-          cp_async4(to, ps);
-          cp_async4(to + 4u, pz);
-          if (GATED) {
-            cp_async4(to + 64u, ps + up);
-            cp_async4(to + 68u, pz + up);
-          }
-          if (--rows_left >= 0) {
-            ps += p.G;
-            pz += p.G;
-          }
+      for (int r = 0; r < (GATED ? 16 : 32); ++r) {
+        // gated: gate row r is row r % 8 of MMA tile r / 8, its up row 8 behind it
+        const uint32_t to = dst + static_cast<uint32_t>((GATED ? (r >> 3) * 16 + (r & 7) : r) * 8);
+        cp_async4(to, ps);
+        cp_async4(to + 4u, pz);
+        if (GATED) {
+          cp_async4(to + 64u, ps + up);
+          cp_async4(to + 68u, pz + up);
+        }
+        if (--rows_left >= 0) {
+          ps += p.G;
+          pz += p.G;
         }
       }
-      stage_x(m0, mt, g_begin + chunk0, chunk);
-      __syncthreads();
-      sum_x(chunk);
-      cp_async_wait_all();
-      __syncthreads();
-      const float2* pa = param + warp * 32 + g8;
-      const float2* sa = sx + 2 * t4;
-      const float* ba = back + 2 * t4;
-      uint32_t xa = x_lane;
-      for (int g0 = 0; g0 < chunk; g0 += DEPTH) {
+    }
+    stage_x(g_begin + chunk0, chunk);
+    __syncthreads();
+    sum_x(chunk);
+    cp_async_wait_all();
+    __syncthreads();
+    const float2* pa = param + warp * 32 + g8;
+    const float2* sa = sx + 2 * t4;
+    const float* ba = back + 2 * t4;
+    uint32_t xa = x_lane;
+    for (int g0 = 0; g0 < chunk; g0 += DEPTH) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-          if (g0 + d >= chunk) break;
-          load((d + DEPTH - 1) % DEPTH, chunk0 + g0 + d + DEPTH - 1);
-          load_x(xa);
-          const float4 sums = *reinterpret_cast<const float4*>(sa);  // two tokens
-          const float2 bk = *reinterpret_cast<const float2*>(ba);
-          float s[2][4];
+      for (int d = 0; d < DEPTH; ++d) {
+        if (g0 + d >= chunk) break;
+        load((d + DEPTH - 1) % DEPTH, chunk0 + g0 + d + DEPTH - 1);
+        load_x(xa);
+        const float4 sums = *reinterpret_cast<const float4*>(sa);  // two tokens
+        const float2 bk = *reinterpret_cast<const float2*>(ba);
+        float s[2][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t lo = word_of(w[d][2 * i], k), hi = word_of(w[d][2 * i + 1], k);
-              const uint32_t l8 = lo >> 8, h8 = hi >> 8;
-              if (k == 0)
-                mma16816_from(s[i], sums.x, sums.z, code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
-              else
-                mma16816(s[i], code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
-              mma16816(s[i], code_even(l8), code_even(h8), code_odd(l8), code_odd(h8), x[k].z, x[k].w);
-            }
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float2 lo = pa[16 * i], hi = pa[16 * i + 8];
-            acc[i][0] = fmaf(lo.x * bk.x, fmaf(lo.y, sums.y, s[i][0]), acc[i][0]);
-            acc[i][1] = fmaf(lo.x * bk.y, fmaf(lo.y, sums.w, s[i][1]), acc[i][1]);
-            acc[i][2] = fmaf(hi.x * bk.x, fmaf(hi.y, sums.y, s[i][2]), acc[i][2]);
-            acc[i][3] = fmaf(hi.x * bk.y, fmaf(hi.y, sums.w, s[i][3]), acc[i][3]);
+            const uint32_t lo = word_of(w[d][2 * i], k), hi = word_of(w[d][2 * i + 1], k);
+            const uint32_t l8 = lo >> 8, h8 = hi >> 8;
+            if (k == 0)
+              mma16816_from(s[i], sums.x, sums.z, code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
+            else
+              mma16816(s[i], code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
+            mma16816(s[i], code_even(l8), code_even(h8), code_odd(l8), code_odd(h8), x[k].z, x[k].w);
           }
-          pa += PARAM_LD;
-          sa += TOKENS;
-          ba += TOKENS;
-          xa += x_group;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 lo = pa[16 * i], hi = pa[16 * i + 8];
+          acc[i][0] = fmaf(lo.x * bk.x, fmaf(lo.y, sums.y, s[i][0]), acc[i][0]);
+          acc[i][1] = fmaf(lo.x * bk.y, fmaf(lo.y, sums.w, s[i][1]), acc[i][1]);
+          acc[i][2] = fmaf(hi.x * bk.x, fmaf(hi.y, sums.y, s[i][2]), acc[i][2]);
+          acc[i][3] = fmaf(hi.x * bk.y, fmaf(hi.y, sums.w, s[i][3]), acc[i][3]);
         }
+        pa += PARAM_LD;
+        sa += TOKENS;
+        ba += TOKENS;
+        xa += x_group;
       }
     }
-
-    // partial sums of this slice; CTA r of the cluster adds and stores the r-th share of the outputs
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float* mine = part + warp * 32 + i * 16 + g8;
-      mine[(2 * t4) * PART_LD] = acc[i][0];
-      mine[(2 * t4 + 1) * PART_LD] = acc[i][1];
-      mine[(2 * t4) * PART_LD + 8] = acc[i][2];
-      mine[(2 * t4 + 1) * PART_LD + 8] = acc[i][3];
-    }
-    if (slices > 1) cluster_sync();
-    else __syncthreads();
-    const uint32_t part_a = smem_u32(part);
-    auto total = [&](int idx) {
-      if (slices == 1) return part[idx];
-      float from[MAX_SLICES];  // all of them on their way before the first is added
-#pragma unroll
-      for (int r = 0; r < MAX_SLICES; ++r)
-        from[r] = r < slices ? ld_cluster_f32(map_to_rank(part_a + static_cast<uint32_t>(idx * 4), r)) : 0.0f;
-      float v = 0.0f;
-#pragma unroll
-      for (int r = 0; r < MAX_SLICES; ++r) v += from[r];
-      return v;
-    };
-    const int share = (OUT_ROWS + slices - 1) / slices;
-    const int first = slice * share;
-    const int n_rows = max(0, min(share, OUT_ROWS - first));
-    for (int i = static_cast<int>(threadIdx.x); i < n_rows * mt; i += THREADS) {
-      const int m = i / n_rows, r = first + i - m * n_rows;
-      const int64_t o = out0 + r;
-      if (o >= n_out) continue;
-      float v;
-      if (GATED) {
-        const int idx = m * PART_LD + (r >> 3) * 16 + (r & 7);
-        const float a = total(idx), b = total(idx + 8);
-        v = silu(a) * b;
-      } else {
-        v = total(m * PART_LD + r);
-        if (p.bias != nullptr) v += bf16_lo(p.bias[o]);
-      }
-      const __nv_bfloat16 y = __float2bfloat16_rn(v);
-      p.Y[(row0 + m0 + m) * p.ldy + o] = *reinterpret_cast<const uint16_t*>(&y);
-    }
-    if (slices > 1) cluster_sync();  // every CTA has read this one's partial sums
-    else __syncthreads();
   }
+
+  // partial sums of this slice; CTA r of the cluster adds and stores the r-th share of the outputs
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float* mine = part + warp * 32 + i * 16 + g8;
+    mine[(2 * t4) * PART_LD] = acc[i][0];
+    mine[(2 * t4 + 1) * PART_LD] = acc[i][1];
+    mine[(2 * t4) * PART_LD + 8] = acc[i][2];
+    mine[(2 * t4 + 1) * PART_LD + 8] = acc[i][3];
+  }
+  if (slices > 1) cluster_sync();
+  else __syncthreads();
+  const uint32_t part_a = smem_u32(part);
+  auto total = [&](int idx) {
+    if (slices == 1) return part[idx];
+    float from[MAX_SLICES];  // all of them on their way before the first is added
+#pragma unroll
+    for (int r = 0; r < MAX_SLICES; ++r)
+      from[r] = r < slices ? ld_cluster_f32(map_to_rank(part_a + static_cast<uint32_t>(idx * 4), r)) : 0.0f;
+    float v = 0.0f;
+#pragma unroll
+    for (int r = 0; r < MAX_SLICES; ++r) v += from[r];
+    return v;
+  };
+  const int share = (OUT_ROWS + slices - 1) / slices;
+  const int first = slice * share;
+  const int n_rows = max(0, min(share, OUT_ROWS - first));
+  for (int i = static_cast<int>(threadIdx.x); i < n_rows * mt; i += THREADS) {
+    const int m = i / n_rows, r = first + i - m * n_rows;
+    const int64_t o = out0 + r;
+    if (o >= n_out) continue;
+    float v;
+    if (GATED) {
+      const int idx = m * PART_LD + (r >> 3) * 16 + (r & 7);
+      const float a = total(idx), b = total(idx + 8);
+      v = silu(a) * b;
+    } else {
+      v = total(m * PART_LD + r);
+      if (p.bias != nullptr) v += bf16_lo(p.bias[o]);
+    }
+    const __nv_bfloat16 y = __float2bfloat16_rn(v);
+    p.Y[(row0 + m) * p.ldy + o] = *reinterpret_cast<const uint16_t*>(&y);
+  }
+  if (slices > 1) cluster_sync();  // every CTA has read this one's partial sums
 }
 
 }  // namespace few
