@@ -41,6 +41,7 @@
 // is bounded.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -69,8 +70,8 @@ constexpr int FIRST_EPI = 4, EPI_WARPS = 8;
 constexpr int FIRST_DQ = 12, DQ_SETS = 2, DQ_WARPS = 4 * DQ_SETS;
 constexpr int THREADS = 32 * (FIRST_DQ + DQ_WARPS);
 // 640 threads x 96 registers at launch; the scaling warps hold 96 sums each
-constexpr int LAUNCH_REGS = 96, EPI_REGS = 152, OTHER_REGS = 56;
-static_assert(32 * (EPI_WARPS * EPI_REGS + (THREADS / 32 - EPI_WARPS) * OTHER_REGS) <= THREADS * LAUNCH_REGS,
+constexpr int LAUNCH_REGS = 96, EPI_REGS = 152, DQ_REGS = 64, ROLE_REGS = 48;
+static_assert(32 * (FIRST_EPI * ROLE_REGS + EPI_WARPS * EPI_REGS + DQ_WARPS * DQ_REGS) <= THREADS * LAUNCH_REGS,
               "the shares fit what the block was launched with");
 constexpr int BLOCK = 32;                         // tokens per load of a scaling warp
 constexpr int CHUNKS = BN / BLOCK / 2;            // blocks per scaling warp
@@ -148,6 +149,11 @@ __device__ __forceinline__ void umma_bf16_pair_ts(uint32_t d_tmem, uint32_t a_tm
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // y += s * v on both fp32 lanes, v given as two registers.
 __device__ __forceinline__ void fma_f32x2(uint64_t& y, uint64_t s, uint32_t lo, uint32_t hi) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(y) : "l"(f32x2_pack(lo, hi)), "l"(s));
@@ -175,15 +181,17 @@ __device__ __forceinline__ uint32_t unpack_pair_any(uint32_t byte, float z) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Bounded wait: the hardware suspends the waiting threads for up to 20 us per try. One that gives up, after the limit or
-// because another has, returns like any other: the roles run on to the end of their tile, where they look at the
-// status, so that a wait costs its poll and one branch in the loops (a result to carry and test cost the scaling warps a
-// third of their instructions).
-constexpr uint32_t SLEEP_NS = 20000;
+// Bounded wait. One that gives up, after the limit or because another has, returns like any other: the roles run on to the
+// end of their tile, where they look at the status, so that a wait costs its poll and one branch in the loops (a result
+// to carry and test cost the scaling warps a third of their instructions). The status and the clock are looked at after 64
+// polls; a time that the hardware may suspend the thread for, given with the poll, cost 2 to 4 % by waking it late.
 __device__ __forceinline__ void wait_slow(uint32_t bar, uint32_t parity, DeviceStatus* st, uint64_t limit, unsigned where) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
-  while (!mbar_try_wait_sleep(bar, parity, SLEEP_NS)) {
+  while (!mbar_try_wait(bar, parity)) {
     if (status_code(st) != 0u) return;
     if (global_timer_ns() - t0 > limit) {
       raise_timeout(st, where);
@@ -192,7 +200,7 @@ __device__ __forceinline__ void wait_slow(uint32_t bar, uint32_t parity, DeviceS
   }
 }
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, const Params& p, unsigned where) {
-  if (!mbar_try_wait_sleep(bar, parity, SLEEP_NS)) wait_slow(bar, parity, p.status, p.limit_ns, where);
+  if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, p.status, p.limit_ns, where);
 }
 
 template <bool GATED>
@@ -217,6 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto parity = [](uint32_t i) { return (i / STAGES) & 1u; };
   auto cfull_bar = [&](int c) { return bar0 + 8u * (2 * STAGES + c); };             // codes and parameters landed
   auto cempty_bar = [&](int c) { return bar0 + 8u * (2 * STAGES + CSTAGES + c); };  // and read
+  const uint32_t full0 = map_to_rank(bar0, 0);  // the even CTA's full_bar(0)
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * CSTAGES);
   const uint32_t smem_base = smem_u32(smem);
   auto x_tile = [&](uint32_t i) { return smem_base + (i % STAGES) * X_BYTES; };
@@ -299,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto tile_at = [&](int t) { return tile_of(t, first_tile, first_row, p.E); };
 
   if (warp < FIRST_EPI) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ROLE_REGS));
     if (warp == 0 && elect_one()) {
       // ------------------------------------------------------------------------------ TMA (token rows)
       uint32_t i = 0;
@@ -313,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int32_t row = tile.row0 + static_cast<int32_t>(rank) * half;
         for (int g = 0; g < num_groups; ++g, ++i) {
           if (i >= STAGES) wait(done_bar(i), parity(i - STAGES), p, kSiteTmaEmpty);
-          const uint32_t fb = map_to_rank(full_bar(i), 0);
+          const uint32_t fb = full0 + 8u * (i % STAGES);
           if (rank == 0) mbar_arrive_expect_tx(full_bar(i), bytes);
           tma_load_2d_pair_hint(x_tile(i), map, g * 2 * BK, row, fb, pol);
           tma_load_2d_pair_hint(x_tile(i) + X_HALF_BYTES, map, g * 2 * BK + BK, row, fb, pol);
@@ -423,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp >= FIRST_DQ) {
     // ------------------------------------------------------------------------------ unpackers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DQ_REGS));
     const int set = (warp - FIRST_DQ) / 4;  // which half of every group
     const int quarter = warp & 3;
     const int r = lane + 32 * quarter;      // the lane's row of the CTA's 128
@@ -432,6 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int slot = 0;
     uint32_t phase = 0, i = 0, buf = 0;
     for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
+#pragma unroll 2  // a slot's two groups: without the tests for them narrow tiles take 4 % less
       for (int g = 0; g < num_groups; ++g, ++i) {
         const int odd = g & 1;  // a slot's second group
         if (!odd) wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
@@ -445,15 +455,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                      : "r"(c_tile(slot) + C_BYTES + P_BYTES + static_cast<uint32_t>(r * 8 + odd * 4))
                      : "memory");
         const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        const bool far = __any_sync(0xffffffffu, !(fabsf(z) <= 240.0f));
+        const __nv_bfloat162 zz = __float2bfloat162_rn(z * -0.015625f);
+        const uint32_t zb = *reinterpret_cast<const uint32_t*>(&zz);
         uint32_t o[32];
-        if (__any_sync(0xffffffffu, !(fabsf(z) <= 240.0f))) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = unpack_pair_any((w[c / 4] >> (8 * (c & 3))) & 0xFFu, z);
-        } else {
-          const __nv_bfloat162 zz = __float2bfloat162_rn(z * -0.015625f);
-          const uint32_t zb = *reinterpret_cast<const uint32_t*>(&zz);
+        for (int c = 0; c < 8; ++c) unpack_word(w[c], zb, o + 4 * c);
+        if (i >= depth) wait(done_bar(i - depth), parity(i - depth), p, kSiteTmaProduced);
+        __syncwarp();
+        tc_fence_after();  // the MMAs that read the buffer come before the stores below
+        tmem_st32(ta + buf * buf_cols, o);
+        if (far) {  // the words again, eight columns at a time
+          tmem_wait_st();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t at = line + (((chunk + static_cast<uint32_t>(c >> 1)) ^ sw) << 4) + static_cast<uint32_t>((c & 1) * 8);
+            uint32_t v[2], f[8];
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
 #pragma unroll
-          for (int c = 0; c < 8; ++c) unpack_word(w[c], zb, o + 4 * c);
+            for (int k = 0; k < 8; ++k) f[k] = unpack_pair_any((v[k / 4] >> (8 * (k & 3))) & 0xFFu, z);
+            tmem_st8(ta + buf * buf_cols + static_cast<uint32_t>(c * 8), f);
+          }
         }
         if (odd || g + 1 == num_groups) {
           __syncwarp();
@@ -463,15 +485,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             phase ^= 1u;
           }
         }
-        if (i >= depth) wait(done_bar(i - depth), parity(i - depth), p, kSiteTmaProduced);
-        __syncwarp();
-        tc_fence_after();  // the MMAs that read the buffer come before the stores below
-        tmem_st32(ta + buf * buf_cols, o);
         if (++buf == depth) buf = 0;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(map_to_rank(full_bar(i), 0));
+        if (lane == 0) mbar_arrive_pair(full0 + 8u * (i % STAGES));
       }
     }
   } else {
@@ -480,7 +498,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, half = (warp - FIRST_EPI) / 4;
     const int r = lane + 32 * quarter;
     int slot = 0;
-    uint32_t phase = 0, i = 0, buf = 0;
+    const uint32_t c_first = c_tile(0) + C_BYTES + static_cast<uint32_t>(r * 8);
+    const uint32_t ta0 = tmem_base + static_cast<uint32_t>(half * BLOCK) + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t phase = 0, i = 0, buf = 0, ct = c_first, ta = ta0;
     if (lane == 0)  // every accumulator is free
       for (uint32_t d = 0; d < depth; ++d) mbar_arrive_pair(map_to_rank(full_bar(d), 0));
     for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
@@ -492,37 +512,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
         for (int k = 0; k < BLOCK / 2; ++k) y[c][k] = 0ull;
-      float2 steps = make_float2(0.0f, 0.0f);
-      for (int g = 0; g < num_groups; ++g, ++i) {
-        if ((g & 1) == 0) {
-          wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
-          steps = few::lds64f(c_tile(slot) + C_BYTES + static_cast<uint32_t>(r * 8));
+      // the tile's groups, for a warp with N blocks (one without any reads a block of no token): a test per block in the loop,
+      // which also kept the accumulator's loads from being moved, cost a tile of 192 tokens a tenth of its time
+      auto scale_groups = [&](auto blocks_c) {
+        constexpr int N = decltype(blocks_c)::value;
+        float2 steps = make_float2(0.0f, 0.0f);
+#pragma unroll (N > 1 ? 1 : 2)
+        for (int g = 0; g < num_groups; ++g, ++i) {
+          if ((g & 1) == 0) {
+            wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
+            steps = few::lds64f(ct);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cempty_bar(slot));
+            ct += CSTAGE_BYTES;
+            if (++slot == CSTAGES) {
+              slot = 0;
+              ct = c_first;
+              phase ^= 1u;
+            }
+          }
+          const uint32_t s64 = __float_as_uint(((g & 1) ? steps.y : steps.x) * 64.0f);
+          const uint64_t ss = f32x2_pack(s64, s64);
+          wait(done_bar(i), parity(i), p, kSiteEpiAccFull);
           __syncwarp();
-          if (lane == 0) mbar_arrive(cempty_bar(slot));
-          if (++slot == CSTAGES) {
-            slot = 0;
-            phase ^= 1u;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            float v[BLOCK];  // columns past the tile's are of no token
+            tmem_ld32(ta + static_cast<uint32_t>(c * 2 * BLOCK), v);
+#pragma unroll
+            for (int k = 0; k < BLOCK / 2; ++k) fma_f32x2(y[c][k], ss, __float_as_uint(v[2 * k]), __float_as_uint(v[2 * k + 1]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(full0 + 8u * ((i + depth) % STAGES));  // the group that overwrites it
+          ta += buf_cols;
+          if (++buf == depth) {
+            buf = 0;
+            ta = ta0;
           }
         }
-        const uint32_t s64 = __float_as_uint(((g & 1) ? steps.y : steps.x) * 64.0f);
-        const uint64_t ss = f32x2_pack(s64, s64);
-        wait(done_bar(i), parity(i), p, kSiteEpiAccFull);
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t ta = tmem_base + buf * buf_cols + static_cast<uint32_t>(half * BLOCK) + (static_cast<uint32_t>(quarter * 32) << 16);
-#pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          if (c >= mine) break;
-          float v[BLOCK];  // columns past the tile's are of no token
-          tmem_ld32(ta + static_cast<uint32_t>(c * 2 * BLOCK), v);
-#pragma unroll
-          for (int k = 0; k < BLOCK / 2; ++k) fma_f32x2(y[c][k], ss, __float_as_uint(v[2 * k]), __float_as_uint(v[2 * k + 1]));
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_pair(map_to_rank(full_bar(i + depth), 0));  // the group that overwrites it
-        if (++buf == depth) buf = 0;
-      }
+      };
+      if (mine >= 3) scale_groups(std::integral_constant<int, 3>{});
+      else if (mine == 2) scale_groups(std::integral_constant<int, 2>{});
+      else scale_groups(std::integral_constant<int, 1>{});
       if (status_code(st) != 0u) break;  // nothing of an unfinished tile is stored
 
       int64_t o, n_out;
