@@ -33,12 +33,19 @@
 //   2      TMA of the code words, 128 rows x 256 in-features at a time (128 bytes of a row), into a ring of its own
 //   3      steps and zero points of those rows and groups by cp.async, counted on the same barrier
 //   4-11   scaling and epilogue: two warps per quarter of the rows, alternate blocks of 32 tokens
-//   12-19  unpackers: two sets of four warps, one for each half of a group, a weight row per lane, into as many
-//          operand buffers
+//   12-19  unpackers: two sets of four warps that take groups in turn, a weight row per lane, into as many operand buffers
 // The thread that issues the MMAs waits once per group: one barrier counts the token rows, the unpacked operand and the
 // reading of the accumulator that the group will overwrite, and one commit per group tells all three that it is done
 // (with a wait and a commit for each, and per 64 in-features, that thread took 1700 cycles per group). Every wait
 // is bounded.
+//
+// Measured (B200): 16384 rows to 32 experts of 4096 -> 2 x 2048, gated, 553 us, 1.0 PFLOP/s; 600 rows to 8 of 14336 -> 4096
+// 155 us; 96 rows to 8 of 4096 -> 2 x 14336, gated, 226 us. Two things bound it. A group's work is short against what surrounds it: the barriers
+// alone, with neither unpacking, scaling, loads nor more than one MMA, take 700 cycles per group, and what counted most
+// was every instruction in the loops of the unpackers and scaling warps (a test per block, the remote barrier's address
+// made anew for each arrival, an unlikely branch before the stores and a poll with a suspend time together cost 742
+// against 581 us for the 16384 rows; unpackers that share each group instead of taking them in turn 581 against 553). And at 192 tokens
+// the accumulators that fit are two, so the scaling of a group has one group's MMAs to hide behind.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -233,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1 + 2 * DQ_WARPS + 2 * EPI_WARPS);  // TMA arm; both CTAs' unpackers and scaling warps
+      mbar_init(full_bar(s), 1 + 2 * 4 + 2 * EPI_WARPS);  // TMA arm; both CTAs' unpackers of the group and scaling warps
       mbar_init(done_bar(s), 1);
     }
     for (int c = 0; c < CSTAGES; ++c) {
@@ -433,63 +440,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp >= FIRST_DQ) {
     // ------------------------------------------------------------------------------ unpackers
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DQ_REGS));
-    const int set = (warp - FIRST_DQ) / 4;  // which half of every group
+    const int set = (warp - FIRST_DQ) / 4;  // takes the groups with g % 2 == set, a slot's first or second
     const int quarter = warp & 3;
     const int r = lane + 32 * quarter;      // the lane's row of the CTA's 128
     const uint32_t sw = static_cast<uint32_t>(r & 7);
-    const uint32_t ta = tmem_base + acc_cols + static_cast<uint32_t>(set * (BK / 2)) + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t ta = tmem_base + acc_cols + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t first = c_tile(0) + static_cast<uint32_t>(r * 128);
+    const uint32_t at0 = (static_cast<uint32_t>(4 * set) ^ sw) << 4, at1 = (static_cast<uint32_t>(4 * set + 1) ^ sw) << 4;
+    const uint32_t at2 = (static_cast<uint32_t>(4 * set + 2) ^ sw) << 4, at3 = (static_cast<uint32_t>(4 * set + 3) ^ sw) << 4;
+    const uint32_t zp = static_cast<uint32_t>(C_BYTES + P_BYTES + set * 4) - static_cast<uint32_t>(r * 120);  // from `line`
     int slot = 0;
-    uint32_t phase = 0, i = 0, buf = 0;
+    uint32_t phase = 0, i = 0;
     for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
-#pragma unroll 2  // a slot's two groups: without the tests for them narrow tiles take 4 % less
-      for (int g = 0; g < num_groups; ++g, ++i) {
-        const int odd = g & 1;  // a slot's second group
-        if (!odd) wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
-        const uint32_t line = c_tile(slot) + static_cast<uint32_t>(r * 128);
-        const uint32_t chunk = static_cast<uint32_t>(4 * odd + 2 * set);
-        const uint4 w0 = few::lds128(line + ((chunk ^ sw) << 4));
-        const uint4 w1 = few::lds128(line + (((chunk + 1u) ^ sw) << 4));
-        float z;
-        asm volatile("ld.shared.f32 %0, [%1];"
-                     : "=f"(z)
-                     : "r"(c_tile(slot) + C_BYTES + P_BYTES + static_cast<uint32_t>(r * 8 + odd * 4))
-                     : "memory");
-        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        const bool far = __any_sync(0xffffffffu, !(fabsf(z) <= 240.0f));
-        const __nv_bfloat162 zz = __float2bfloat162_rn(z * -0.015625f);
-        const uint32_t zb = *reinterpret_cast<const uint32_t*>(&zz);
-        uint32_t o[32];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) unpack_word(w[c], zb, o + 4 * c);
-        if (i >= depth) wait(done_bar(i - depth), parity(i - depth), p, kSiteTmaProduced);
-        __syncwarp();
-        tc_fence_after();  // the MMAs that read the buffer come before the stores below
-        tmem_st32(ta + buf * buf_cols, o);
-        if (far) {  // the words again, eight columns at a time
-          tmem_wait_st();
+      uint32_t buf = (i + static_cast<uint32_t>(set)) % depth;
+      uint32_t n = i + static_cast<uint32_t>(set);
+      i += static_cast<uint32_t>(num_groups);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t at = line + (((chunk + static_cast<uint32_t>(c >> 1)) ^ sw) << 4) + static_cast<uint32_t>((c & 1) * 8);
-            uint32_t v[2], f[8];
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+      for (int j = 0; j < num_slots; ++j) {
+        wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
+        if (n != i) {  // the last slot may hold one group
+          const uint32_t line = first + static_cast<uint32_t>(slot * CSTAGE_BYTES);
+          float z;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(line + zp) : "memory");
+          const bool far = __any_sync(0xffffffffu, !(fabsf(z) <= 240.0f));
+          const __nv_bfloat162 zz = __float2bfloat162_rn(z * -0.015625f);
+          const uint32_t zb = *reinterpret_cast<const uint32_t*>(&zz);
+          const uint32_t to = ta + buf * buf_cols;
+          buf += 2;
+          if (buf >= depth) buf -= depth;
+          uint32_t o[32];
+          {
+            const uint4 w0 = few::lds128(line + at0), w1 = few::lds128(line + at1);
+            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = unpack_pair_any((v[k / 4] >> (8 * (k & 3))) & 0xFFu, z);
-            tmem_st8(ta + buf * buf_cols + static_cast<uint32_t>(c * 8), f);
+            for (int c = 0; c < 8; ++c) unpack_word(w[c], zb, o + 4 * c);
           }
-        }
-        if (odd || g + 1 == num_groups) {
+          const uint4 w0 = few::lds128(line + at2), w1 = few::lds128(line + at3);
+          if (n >= depth) wait(done_bar(n - depth), parity(n - depth), p, kSiteTmaProduced);
           __syncwarp();
-          if (lane == 0) mbar_arrive(cempty_bar(slot));
-          if (++slot == CSTAGES) {
-            slot = 0;
-            phase ^= 1u;
+          tc_fence_after();  // the MMAs that read the buffer come before the stores below
+          tmem_st32(to, o);
+          {
+            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int c = 0; c < 8; ++c) unpack_word(w[c], zb, o + 4 * c);
           }
+          tmem_st32(to + 32u, o);
+          if (far) {  // the words again, eight columns at a time
+            tmem_wait_st();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              const uint32_t at = line + (((static_cast<uint32_t>(4 * set + (c >> 1))) ^ sw) << 4) + static_cast<uint32_t>((c & 1) * 8);
+              uint32_t v[2], f[8];
+              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+#pragma unroll
+              for (int k = 0; k < 8; ++k) f[k] = unpack_pair_any((v[k / 4] >> (8 * (k & 3))) & 0xFFu, z);
+              tmem_st8(to + static_cast<uint32_t>(c * 8), f);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(full0 + 8u * (n % STAGES));
+          n += 2;
         }
-        if (++buf == depth) buf = 0;
-        tmem_wait_st();
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(full0 + 8u * (i % STAGES));
+        if (lane == 0) mbar_arrive(cempty_bar(slot));
+        if (++slot == CSTAGES) {
+          slot = 0;
+          phase ^= 1u;
+        }
       }
     }
   } else {
