@@ -382,3 +382,35 @@ def test_quantize_experts_matches_each_layer():
         ref = X[(order[a:b].long() // k).cuda()].double() @ W[e].double().T
         mse = float(((Y[a:b].double() - ref) ** 2).mean())
         assert mse <= 1.25 * float(out["losses"][e].min()) + 2.0 ** -16 * float((ref ** 2).mean())
+
+
+@pytest.mark.parametrize("counts", [[3, 8], [4, 30], [200, 5]])
+@pytest.mark.parametrize("gated", [False, True])
+def test_nonfinite_rows_stay_apart(counts, gated):
+    """A row with an infinity or a NaN changes no other row's bits, and its own outputs say so."""
+    K, O, R = 640, 136, sum(counts)
+    _, W = expert_weights(2, O, K, 60)
+    X = normal((R, K), 61).cuda()
+    offsets = offsets_of(counts).cuda()
+    clean = awq.w4a16_experts(X, offsets, *W, gated=gated)
+    bad = {1: float("nan"), counts[0] - 1: float("inf"), R - 2: -float("inf")}
+    for row, value in bad.items():
+        X[row, 77 + row] = value
+    got = awq.w4a16_experts(X, offsets, *W, gated=gated)
+    others = [r for r in range(R) if r not in bad]
+    assert torch.equal(got[others], clean[others])
+    if not gated:  # (an infinite gate may leave silu(gate) = 0)
+        assert not bool(torch.isfinite(got[list(bad)]).any())
+
+
+def test_offsets_out_of_order_stay_inside():
+    """Offsets that no sort gives, falling, negative and past the rows: nothing outside Y's rows and columns is written."""
+    K, O, R = 256, 72, 40
+    _, W = expert_weights(4, O, K, 62)
+    X = normal((R, K), 63).cuda()
+    for offsets in ([-5, 20, 3, 1000000000, 2], [40, 30, 20, 10, 0], [2147483647] * 5, [-2147483648, 0, 12, 7, 40]):
+        buf = torch.full((R + 2, O + 2), 7.0, dtype=torch.bfloat16, device="cuda")
+        awq.w4a16_experts(X, torch.tensor(offsets, dtype=torch.int32, device="cuda"), *W, out=buf[1:-1, 1:-1])
+        keep = torch.ones_like(buf, dtype=torch.bool)
+        keep[1:-1, 1:-1] = False
+        assert bool((buf[keep] == 7.0).all())
