@@ -343,13 +343,22 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   q.pair_params = q.G % 2 == 0 && ((reinterpret_cast<uintptr_t>(steps) | reinterpret_cast<uintptr_t>(zeros)) & 7u) == 0;
   q.status = static_cast<awq::DeviceStatus*>(workspace);
   q.limit_ns = g_wait_limit_ns.load();
-  const unsigned ctas = static_cast<unsigned>(2 * d->expert_clusters);
+  // The two kernels write different rows, so the second starts as the first one's SMs fall free (an empty grouped kernel
+  // costs 8 us by itself).
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * d->expert_clusters));
+  cfg.blockDim = dim3(awq::grp::THREADS);
+  cfg.dynamicSmemBytes = awq::grp::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (gated)
-    awq::grp::w4a16_experts_kernel<true><<<ctas, awq::grp::THREADS, awq::grp::SMEM_BYTES, st>>>(tmX[0], tmX[1], tmX[2],
-                                                                                                  tmC, q);
+    AWQ_CUDA(cudaLaunchKernelEx(&cfg, awq::grp::w4a16_experts_kernel<true>, tmX[0], tmX[1], tmX[2], tmC, q));
   else
-    awq::grp::w4a16_experts_kernel<false><<<ctas, awq::grp::THREADS, awq::grp::SMEM_BYTES, st>>>(tmX[0], tmX[1], tmX[2],
-                                                                                                  tmC, q);
+    AWQ_CUDA(cudaLaunchKernelEx(&cfg, awq::grp::w4a16_experts_kernel<false>, tmX[0], tmX[1], tmX[2], tmC, q));
   AWQ_TRY(check_launch("w4a16_experts_kernel"));
   return ok();
 }

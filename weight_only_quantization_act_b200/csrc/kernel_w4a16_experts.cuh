@@ -629,6 +629,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
+  // Launched while the few-token kernel's last CTAs run: what follows this kernel on the stream has to wait for both.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace grp

@@ -145,6 +145,8 @@ __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __e
 template <bool GATED>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  // The experts' grouped kernel reads nothing that this one writes: it may start once every CTA of this one has.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
   const int slice = static_cast<int>(blockIdx.x), slices = static_cast<int>(gridDim.x);
