@@ -357,7 +357,8 @@ AWQ_API awq_status awq_expert_combine_backward(const void *dY, int64_t T, int64_
  * their exact value, (q - z) summed per group and scaled by the fp32 step; only in a group with |z| > 240 (its
  * weights nearly equal) an expert with more than 8 rows takes q - z rounded to bf16.
  *   Xs      device bf16 [R, K] sorted rows, row stride ldx (multiple of 8)
- *   codes   device uint32 [E, O, K/8], 16-byte aligned; steps / zeros device float [E, O, K/128]
+ *   codes   device uint32 [E, O, K/8], 16-byte aligned; steps / zeros device float [E, O, K/128] (as packed:
+ *           integer-valued zeros)
  *   Y       device bf16 [R, O] (gated: [R, O/2]), row stride ldy >= its columns; rows from offsets[E] on are left
  *           as they were; must not overlap Xs
  *   workspace  device, 16-byte aligned, >= awq_w4a16_experts_workspace_size(R, E, K, O) bytes, ZERO-FILLED
