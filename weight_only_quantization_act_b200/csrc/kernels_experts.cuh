@@ -254,37 +254,40 @@ __global__ void __launch_bounds__(ROW_THREADS) expert_gather_scaled_kernel(
     const uint16_t* __restrict__ X, int64_t ldx, int64_t T, int64_t K, const int* __restrict__ offsets, int E,
     const int* __restrict__ order, int top_k, const float* __restrict__ scales, uint16_t* __restrict__ Xs, int64_t ldxs,
     int64_t n_rows) {
-  __shared__ int slots[RUN], experts[RUN], first[MAX_EXPERTS];
+  __shared__ const uint16_t* rows[RUN];  // of X; null where no slot stands
+  __shared__ int experts[RUN], first[MAX_EXPERTS];
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * RUN;
   for (int e = threadIdx.x; e < E; e += ROW_THREADS) first[e] = __ldg(offsets + e);
   int my_slot = -1;
   if (threadIdx.x < RUN && r0 + threadIdx.x < n_rows) my_slot = __ldg(order + r0 + threadIdx.x);
   __syncthreads();
   if (threadIdx.x < RUN) {
-    if (my_slot >= T * top_k) my_slot = -1;
-    slots[threadIdx.x] = my_slot;
-    experts[threadIdx.x] = my_slot >= 0 ? expert_of_row(first, E, static_cast<int>(r0 + threadIdx.x)) : -1;
+    const bool real = my_slot >= 0 && my_slot < T * top_k;
+    rows[threadIdx.x] = real ? X + static_cast<int64_t>(my_slot / top_k) * ldx : nullptr;
+    experts[threadIdx.x] = real ? expert_of_row(first, E, static_cast<int>(r0 + threadIdx.x)) : -1;
   }
   __syncthreads();
   const int64_t c = static_cast<int64_t>(blockIdx.y) * ROW_THREADS + threadIdx.x;
   if (c >= K / 8) return;
   uint64_t below[4], above[4];  // r- and r+ of two columns each
+  const float* sc = nullptr;    // the expert's scales
   bool divide = false;          // a scale whose reciprocal is no normal number
   int have = -1;
+  uint16_t* dst = Xs + r0 * ldxs + c * 8;
 #pragma unroll 1
   for (int i0 = 0; i0 < RUN; i0 += AT_ONCE) {
     uint4 v[AT_ONCE];
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i)
-      if (slots[i0 + i] >= 0) v[i] = ld_row(X + static_cast<int64_t>(slots[i0 + i] / top_k) * ldx, c);
+      if (rows[i0 + i] != nullptr) v[i] = ld_row(rows[i0 + i], c);
 #pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) {
-      if (slots[i0 + i] < 0) continue;
+    for (int i = 0; i < AT_ONCE; ++i, dst += ldxs) {
       const int e = experts[i0 + i];
-      const float* sc = scales + e * K + c * 8;
+      if (e < 0) continue;
       if (e != have) {
         have = e;
         divide = false;
+        sc = scales + e * K + c * 8;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 two = __ldg(reinterpret_cast<const float2*>(sc) + k);
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(ROW_THREADS) expert_gather_scaled_kernel(
         q[2] = exact.z;
         q[3] = exact.w;
       }
-      *reinterpret_cast<uint4*>(Xs + (r0 + i0 + i) * ldxs + c * 8) = make_uint4(q[0], q[1], q[2], q[3]);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
     }
   }
 }
