@@ -63,7 +63,8 @@ awq_status launch_few(awq::few::Params& p, int64_t E, int64_t active, int64_t to
   p.g_per = static_cast<int>((p.G + slices - 1) / slices);
   slices = (p.G + p.g_per - 1) / p.g_per;
   p.mp_log2 = tokens <= 1 ? 0 : tokens <= 2 ? 1 : tokens <= 4 ? 2 : 3;
-  p.xg = std::min((p.g_per + awq::few::DEPTH - 1) / awq::few::DEPTH * awq::few::DEPTH, awq::few::chunk_groups(1 << p.mp_log2));
+  const int most = awq::few::chunk_groups(1 << p.mp_log2), chunks = (p.g_per + most - 1) / most;
+  p.xg = ((p.g_per + chunks - 1) / chunks + awq::few::DEPTH - 1) / awq::few::DEPTH * awq::few::DEPTH;  // equal chunks
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(slices), static_cast<unsigned>(n_rb), static_cast<unsigned>(E));
   cfg.blockDim = dim3(awq::few::THREADS);

@@ -52,16 +52,24 @@ constexpr int CTAS_PER_SM = 3;
 constexpr int PART_LD = ROWS + 4;                      // partial sums [TOKENS][PART_LD]
 constexpr int PART_BYTES = TOKENS * PART_LD * 4;
 constexpr int PARAM_LD = ROWS + 1;                     // steps and zero points [group][PARAM_LD], written down a column
-constexpr int CHUNK = 32;                              // groups per chunk of X, 16 for 8 tokens: multiples of DEPTH
+constexpr int CHUNK_BYTES = 54 * 1024;                 // shared memory of a CTA, nearly all for a chunk of groups
 constexpr int MAX_SLICES = 8;                          // portable cluster size
 
 // Shared memory for chunks of `xg` groups of `mp` tokens (mp = 1, 2, 4 or 8).
 __host__ __device__ constexpr int smem_bytes(int xg, int mp) {
   return PART_BYTES + xg * 256 * mp + (xg * PARAM_LD + 1) / 2 * 16 + xg * TOKENS * 12;
 }
-__host__ __device__ constexpr int chunk_groups(int mp) { return mp <= 2 ? CHUNK : mp == 4 ? 24 : 16; }
-constexpr int SMEM_MAX = smem_bytes(CHUNK, 2);
-static_assert(SMEM_MAX >= smem_bytes(16, 8) && SMEM_MAX >= smem_bytes(24, 4) && (SMEM_MAX + 1024) * CTAS_PER_SM <= 228 * 1024,
+// The most groups that fit: what precedes a chunk's first group (its X, steps and zero points on their way, the sums of X)
+// leaves the loads of the codes with the three groups ahead, so few, long and equal chunks
+// (17 groups of 5 tokens as one chunk of 20 and not 16 + 1: 20.6 to 19.7 us). With 74 KB per CTA the L1 that remains holds too few
+// loads: 28672 -> 8192 for 8 tokens 46 to 55 us.
+__host__ __device__ constexpr int chunk_groups(int mp) {
+  return (CHUNK_BYTES - PART_BYTES) / (256 * mp + 8 * PARAM_LD + TOKENS * 12) / DEPTH * DEPTH;
+}
+constexpr int SMEM_MAX = CHUNK_BYTES;
+static_assert(smem_bytes(chunk_groups(1), 1) <= SMEM_MAX && smem_bytes(chunk_groups(2), 2) <= SMEM_MAX &&
+                  smem_bytes(chunk_groups(4), 4) <= SMEM_MAX && smem_bytes(chunk_groups(8), 8) <= SMEM_MAX &&
+                  (SMEM_MAX + 1024) * CTAS_PER_SM <= 228 * 1024,
               "the largest chunk");
 
 struct Params {
@@ -276,13 +284,13 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
   for (int chunk0 = 0; chunk0 < n_groups; chunk0 += p.xg) {
     const int chunk = min(p.xg, n_groups - chunk0);
     __syncthreads();  // the previous chunk has been read
-    if (lane < chunk) {  // steps and zero points, a row of this warp's at a time: a row's groups are neighbours
-      const int64_t first = (e * p.O + weight_row(0)) * p.G + g_begin + chunk0 + lane;
+    for (int gl = lane; gl < chunk; gl += 32) {  // steps and zero points, a row of this warp's at a time: a row's groups are neighbours
+      const int64_t first = (e * p.O + weight_row(0)) * p.G + g_begin + chunk0 + gl;
       const float* ps = p.steps + first;
       const float* pz = p.zeros + first;
       const int64_t up = n_out * p.G;                            // gated: from a gate row to its up row
       int rows_left = static_cast<int>(min(n_out - 1 - weight_row(0), int64_t(32)));  // rows past the end: the last one's
-      uint32_t dst = smem_u32(param + lane * PARAM_LD + warp * 32);
+      uint32_t dst = smem_u32(param + gl * PARAM_LD + warp * 32);
 #pragma unroll 4
       for (int r = 0; r < (GATED ? 16 : 32); ++r) {
         // gated: gate row r is row r % 8 of MMA tile r / 8, its up row 8 behind it
