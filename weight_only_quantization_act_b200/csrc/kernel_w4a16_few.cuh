@@ -28,11 +28,12 @@
 // add their fp32 partial sums through distributed shared memory in slice order: one launch, no workspace, the same
 // result every time.
 //
-// Measured (B200, one call after another, weights of one token and of 8 experts with 2 rows each): 28672 -> 8192 in 34 us and
-// 8 x (4096 -> 2 x 14336) in 145 us, 3.9 and 3.6 TB/s of packed weights. What bounds it is how many loads the SM keeps in
-// flight and how they fall on DRAM pages: with one group ahead and 4 CTAs per SM 36 and 201 us, with three ahead and 4 CTAs
-// (which spills, and opens more rows at once) 36 and 235, with seven ahead and 2 CTAs 35 and 163; with a bulk prefetch of
-// each row into L2 instead 36 and 201; without the loads, the rest takes 25 and 108.
+// Measured (B200, weights of one token and of 8 experts with 2 rows each): 28672 -> 8192 in 32 us in a graph and
+// 8 x (4096 -> 2 x 14336) in 135 us by itself, 4.1 and 3.9 TB/s of packed weights. What bounds it is how many loads the SM
+// keeps in flight and how they fall on DRAM pages, then the instructions between them: with one group ahead and 4 CTAs per SM
+// 36 and 201 us, with three ahead and 4 CTAs (which spills, and opens more rows at once) 36 and 235, with seven ahead and 2
+// CTAs 35 and 163, with four ahead 32 and 143; with a bulk prefetch of each row into L2 instead 36 and 201; with a predicate
+// per load of X and addresses made per group 33 and 142; without the loads, the rest took 25 and 108.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -153,6 +154,8 @@ __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __e
 template <bool GATED>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint4 zero;  // X of tokens past mp
+  if (threadIdx.x == 0) zero = make_uint4(0u, 0u, 0u, 0u);
   // The experts' grouped kernel reads nothing that this one writes: it may start once every CTA of this one has.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -194,10 +197,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
 #pragma unroll
   for (int j = 0; j < 4; ++j) code[j] = codes + weight_row(g8 + 8 * j) * (p.K / 8) + t4 * 4;
   uint4 w[DEPTH][4];
-  auto load = [&](int d, int g) {
-    if (g < n_groups) {
+  int left = n_groups;  // from the groups that `code` stands at
+  auto load = [&](int d, int ahead) {
+    if (ahead < left) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[d][j] = ldg_codes(code[j] + g * 16);
+      for (int j = 0; j < 4; ++j) w[d][j] = ldg_codes(code[j] + ahead * 16);
     }
   };
 
@@ -245,20 +249,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
       }
     }
   };
-  // The B operand of in-features 8 w.. of a group: lanes of tokens past mp load nothing and keep their zeros.
-  const uint32_t x_lane = smem_u32(xs) + static_cast<uint32_t>(((g8 * 4) + t4) * 16);
-  const uint32_t x_real = g8 < mp ? 1u : 0u;
-  const uint32_t x_word = static_cast<uint32_t>(mp * 64), x_group = static_cast<uint32_t>(mp * 256);
+  // The B operand of in-features 8 w.. of a group: lanes of tokens past mp read a zero that stays where it is.
+  const bool x_real = g8 < mp;
+  const uint32_t x_lane = x_real ? smem_u32(xs) + static_cast<uint32_t>(((g8 * 4) + t4) * 16) : smem_u32(&zero);
+  const uint32_t x_word = x_real ? static_cast<uint32_t>(mp * 64) : 0u, x_group = 4 * x_word;
   uint4 x[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = make_uint4(0u, 0u, 0u, 0u);
   auto load_x = [&](uint32_t at) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-                   : "+r"(x[k].x), "+r"(x[k].y), "+r"(x[k].z), "+r"(x[k].w)
-                   : "r"(at + k * x_word), "r"(x_real)
-                   : "memory");
+    for (int k = 0; k < 4; ++k) x[k] = lds128(at + k * x_word);
   };
   // Per group and token what the constants add (rows 0-7 of the tile: 1024 or 64 per in-feature) and the sum of xs (rows
   // 8-15), both with the sign that takes them off.
@@ -320,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) {
         if (g0 + d >= chunk) break;
-        load((d + DEPTH - 1) % DEPTH, chunk0 + g0 + d + DEPTH - 1);
+        load((d + DEPTH - 1) % DEPTH, d + DEPTH - 1);
         load_x(xa);
         const float4 sums = *reinterpret_cast<const float4*>(sa);  // two tokens
         const float2 bk = *reinterpret_cast<const float2*>(ba);
@@ -350,6 +348,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
         ba += TOKENS;
         xa += x_group;
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) code[j] += DEPTH * 16;
+      left -= DEPTH;
     }
   }
 
