@@ -211,7 +211,7 @@ def offsets_of(counts):
     return torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32)
 
 
-FEW_ROWS = 8  # the weights of an expert with more rows enter as q - z in bf16
+FEW_ROWS = 8  # an expert with more rows takes q - z of a zero point beyond +-240 rounded to bf16
 
 
 def check_experts(Xs, counts, parts, got, gated):

@@ -39,13 +39,14 @@
 // (with a wait and a commit for each, and per 64 in-features, that thread took 1700 cycles per group). Every wait
 // is bounded.
 //
-// Measured (B200): 16384 rows to 32 experts of 4096 -> 2 x 2048, gated, 553 us, 1.0 PFLOP/s; 600 rows to 8 of 14336 -> 4096
-// 155 us; 96 rows to 8 of 4096 -> 2 x 14336, gated, 226 us. Two things bound it. A group's work is short against what surrounds it: the barriers
-// alone, with neither unpacking, scaling, loads nor more than one MMA, take 700 cycles per group, and what counted most
-// was every instruction in the loops of the unpackers and scaling warps (a test per block, the remote barrier's address
-// made anew for each arrival, an unlikely branch before the stores and a poll with a suspend time together cost 742
-// against 581 us for the 16384 rows; unpackers that share each group instead of taking them in turn 581 against 553). And at 192 tokens
-// the accumulators that fit are two, so the scaling of a group has one group's MMAs to hide behind.
+// Measured (B200): 16384 rows to 32 experts of 4096 -> 2 x 2048, gated, 553 us, 1.0 PFLOP/s; 600 rows to 8 of
+// 14336 -> 4096 155 us; 96 rows to 8 of 4096 -> 2 x 14336, gated, 221 us. Two things bound it. A group's work is short
+// against what surrounds it: the barriers alone, with neither unpacking, scaling, loads nor more than one MMA, take 700
+// cycles per group, and what counted most was every instruction in the loops of the unpackers and scaling warps (a test
+// per block, the remote barrier's address made anew for each arrival, an unlikely branch before the stores and a poll
+// with a suspend time together cost 742 against 581 us for the 16384 rows; unpackers that share each group instead of
+// taking them in turn 581 against 553). And at 192 tokens the accumulators that fit are two, so the scaling of a group
+// has one group's MMAs to hide behind.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -490,7 +491,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tmem_wait_st();
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
-              const uint32_t at = line + (((static_cast<uint32_t>(4 * set + (c >> 1))) ^ sw) << 4) + static_cast<uint32_t>((c & 1) * 8);
+              const uint32_t at =
+                  line + ((static_cast<uint32_t>(4 * set + (c >> 1)) ^ sw) << 4) + static_cast<uint32_t>((c & 1) * 8);
               uint32_t v[2], f[8];
               asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
 #pragma unroll

@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
   for (int chunk0 = 0; chunk0 < n_groups; chunk0 += p.xg) {
     const int chunk = min(p.xg, n_groups - chunk0);
     __syncthreads();  // the previous chunk has been read
-    for (int gl = lane; gl < chunk; gl += 32) {  // steps and zero points, a row of this warp's at a time: a row's groups are neighbours
+    // steps and zero points, a row of this warp's at a time: a row's groups are neighbours
+    for (int gl = lane; gl < chunk; gl += 32) {
       const int64_t first = (e * p.O + weight_row(0)) * p.G + g_begin + chunk0 + gl;
       const float* ps = p.steps + first;
       const float* pz = p.zeros + first;
