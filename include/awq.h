@@ -299,7 +299,8 @@ AWQ_API awq_status awq_w4a16_gemm(const void *X, int64_t M, int64_t K, int64_t l
  *   bias    device bf16 [O] or NULL (NULL when gated)
  *   Y       device bf16, row stride ldy >= its columns (no alignment beyond 2 bytes); must not overlap X
  * Requires 1 <= M <= AWQ_GEMV_MAX_TOKENS, K % 128 == 0, any O >= 1 (gated: even; at most 8388480 rows, half
- * of that per projection when gated). Deterministic.
+ * of that per projection when gated). Deterministic. An infinity or a NaN in a row of X makes of that row's outputs what the
+ * formula makes of it, and of no other's (so in awq_w4a16_experts too).
  * ------------------------------------------------------------------------------------------------- */
 #define AWQ_GEMV_MAX_TOKENS 8
 AWQ_API awq_status awq_w4a16_gemv(const void *X, int64_t M, int64_t K, int64_t ldx, const uint32_t *codes,

@@ -154,8 +154,12 @@ __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __e
 template <bool GATED>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint4 zero;  // X of tokens past mp
-  if (threadIdx.x == 0) zero = make_uint4(0u, 0u, 0u, 0u);
+  __shared__ uint4 zero;      // X of tokens past mp
+  __shared__ unsigned apart;  // bit m: token m holds an infinity or a NaN in this slice
+  if (threadIdx.x == 0) {
+    zero = make_uint4(0u, 0u, 0u, 0u);
+    apart = 0u;
+  }
   // The experts' grouped kernel reads nothing that this one writes: it may start once every CTA of this one has.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -244,7 +248,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
           const int mk = to[k] >> 16, ck = to[k] & 0xFFFF;
           const int grp = ck >> 4, t = (ck >> 2) & 3, word = ck & 3;
           *reinterpret_cast<uint4*>(xs + (((grp * 4 + word) * mp + mk) * 4 + t) * 16) = *reinterpret_cast<const uint4*>(h);
-          if ((ck & 15) == 0) back[grp * TOKENS + mk] = __uint_as_float((254u - field) << 23);
+          if ((ck & 15) == 0) {
+            back[grp * TOKENS + mk] = __uint_as_float((254u - field) << 23);
+            if (most == 0x7F80u) atomicOr(&apart, 1u << mk);
+          }
         }
       }
     }
@@ -363,6 +370,37 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
     mine[(2 * t4 + 1) * PART_LD] = acc[i][1];
     mine[(2 * t4) * PART_LD + 8] = acc[i][2];
     mine[(2 * t4 + 1) * PART_LD + 8] = acc[i][3];
+  }
+  // What the group sums cannot give, since they take z sum x off sum q x: tokens with an infinity or a NaN again, term by
+  // term from the weights as fp32 numbers, so that each output is the infinity or the NaN of the definition (as in the
+  // experts' grouped kernel). A column of the MMA is a token, so the others have not been touched.
+  const unsigned tokens_apart = apart;
+  if (tokens_apart != 0u) {
+    __syncwarp();
+#pragma unroll 1
+    for (unsigned rest = tokens_apart; rest != 0u; rest &= rest - 1u) {
+      const int m = __ffs(rest) - 1;
+      const uint16_t* xr = p.X + (row0 + m) * p.ldx + static_cast<int64_t>(g_begin) * 128 + lane * 4;
+#pragma unroll 1
+      for (int r = 0; r < 32; ++r) {
+        const int64_t wr = weight_row(r), first = (e * p.O + wr) * p.G + g_begin;
+        const uint32_t* c = codes + wr * (p.K / 8) + (lane >> 1);
+        float v = 0.0f;
+#pragma unroll 1
+        for (int g = 0; g < n_groups; ++g) {
+          const uint2 x4 = *reinterpret_cast<const uint2*>(xr + g * 128);
+          const uint32_t q = c[g * 16] >> ((lane & 1) * 16);
+          const float step = p.steps[first + g], z = p.zeros[first + g];
+          v = fmaf((static_cast<float>(q & 15u) - z) * step, bf16_lo(x4.x), v);
+          v = fmaf((static_cast<float>((q >> 4) & 15u) - z) * step, bf16_hi(x4.x), v);
+          v = fmaf((static_cast<float>((q >> 8) & 15u) - z) * step, bf16_lo(x4.y), v);
+          v = fmaf((static_cast<float>((q >> 12) & 15u) - z) * step, bf16_hi(x4.y), v);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if (lane == 0) part[m * PART_LD + warp * 32 + r] = v;
+      }
+    }
   }
   if (slices > 1) cluster_sync();
   else __syncthreads();
