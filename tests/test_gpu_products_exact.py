@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from tests import _experts_plain as plain
+from tests import _products_bounds as bounds
 from tests.test_gpu_experts import expert_weights, normal, offsets_of
 from weight_only_quantization_act_b200 import awq
 
@@ -54,3 +55,53 @@ def test_infinities_are_those_of_the_definition(rows, gated, K):
         assert torch.equal(got.isinf(), ref.isinf())
         assert torch.equal(got[ref.isinf()], ref[ref.isinf()])
     assert bool(ref.isinf().any())  # the case shows it: not every output is a NaN
+
+
+def weights_around_zero(O, K, seed):
+    """Codes and zero points as packing gives them for normal weights."""
+    codes, steps, zeros = plain.packed(O, K, seed)
+    return codes, steps, torch.where(zeros > 7, 8.0, 7.0)
+
+
+@pytest.mark.parametrize("M,K,O", [(1, 4096, 4096), (8, 28672, 520), (3, 33408, 1400), (5, 1408, 2000), (8, 128, 1000)])
+@pytest.mark.parametrize("one_sided", [False, True])
+def test_few_tokens_lose_nothing_before_the_rounding(M, K, O, one_sided):
+    """Centred activations and those of a ReLU, which are all of one sign: the sums of x do not cancel there."""
+    X = normal((M, K), 92).abs() if one_sided else normal((M, K), 92)
+    W = weights_around_zero(O, K, 93)
+    ref, err = bounds.few(X, *W)
+    got = awq.w4a16_gemv(X.cuda(), *(t.cuda() for t in W))
+    bounds.assert_rounds(got, ref)
+    plain.assert_within(got, ref, err)
+
+
+def test_few_rows_of_experts_lose_nothing_before_the_rounding():
+    counts, K, O = [1, 8, 0, 5], 14336, 600
+    parts = [weights_around_zero(O, K, 94 + e) for e in range(4)]
+    W = tuple(torch.stack([p[i] for p in parts]).cuda() for i in range(3))
+    X = normal((14, K), 95).abs()
+    got = awq.w4a16_experts(X.cuda(), offsets_of(counts).cuda(), *W)
+    for e, (a, b) in enumerate(((0, 1), (1, 9), (9, 9), (9, 14))):
+        if b > a:
+            bounds.assert_rounds(got[a:b], bounds.few(X[a:b], *parts[e])[0])
+
+
+def test_few_tokens_of_any_size():
+    """Powers of two in X come out as they went in; the largest and the smallest stay within the bound."""
+    M, K, O = 4, 768, 300
+    X, W = normal((M, K), 96), plain.packed(O, K, 97)
+    Wd = tuple(t.cuda() for t in W)
+    base = awq.w4a16_gemv(X.cuda(), *Wd)
+    for k in (-96, -40, 60, 112):
+        assert torch.equal(awq.w4a16_gemv((X.double() * 2.0 ** k).bfloat16().cuda(), *Wd).double(), base.double() * 2.0 ** k), k
+    for k in (-128, -118, 117, 121):
+        Xk = (X.double() * 2.0 ** k).bfloat16()
+        ref, err = bounds.few(Xk, *W)
+        plain.assert_within(awq.w4a16_gemv(Xk.cuda(), *Wd), ref, torch.maximum(err, bounds.term_by_term(Xk, *W)[1]))
+    # one token large, the others keep their bits; one group large, the others of the token count
+    X2 = X.clone()
+    X2[1, 200] = 2.0 ** 119
+    got = awq.w4a16_gemv(X2.cuda(), *Wd)
+    assert torch.equal(got[[0, 2, 3]], base[[0, 2, 3]])
+    ref, err = bounds.term_by_term(X2[1:2], *W)
+    plain.assert_within(got[1:2], ref, err)

@@ -5,12 +5,13 @@
 // Mathematics: per group g of 128 in-features and token m, with a power of two c[m, g] that brings the group's largest
 // |x'| to 2^14..2^15 and xs = c x',
 //   Y[m, o] = sum_g step[o, g] / c[m, g] (sum_{k in g} q[o, k] xs[m, k] - z[o, g] sum_{k in g} xs[m, k]).
-// A nibble in place under the exponent bits of 1024 (bits 0-3) or of 64 (bits 4-7) is the fp16 number 1024 + q or 64 + q,
-// so one AND-OR per two codes and one shift per eight make the operand; what the constants add, 1024 or 64 times sums of
-// xs, is taken off per group and token by starting the accumulator there. xs is exact in fp16 down to 2^-31 of the
-// group's largest value and below that off by 2^-40 of it, so the weights enter with their exact value; the tensor
-// cores sum in fp32, the step and zero point are applied once per group and output in fp32. (bf16 patterns 128 + q need a
-// shift for every pair of codes.)
+// A nibble in place in bits 0-3 of a half-word is the fp16 subnormal q 2^-24, in bits 4-7 q 2^-20, so one AND per two codes
+// and one shift per eight make the operand. xs of the in-features that meet the latter is stored as xs / 16, so every term
+// counts 2^-24, and the 2^24 goes into 1 / c. A bf16 x is exact in fp16 down to 2^-28 of its group's largest and below that
+// off by 2^-35 of it, so the weights enter with their exact value; the tensor cores sum 15 |xs| at most in fp32, the step
+// and zero point are applied once per group and output in fp32. (Nibbles under the exponent of 1024 or 64, 1024 + q, take as
+// many instructions, but their sums of 1024 xs have to be taken off again: for one-sided X, a ReLU's for one, up to 1e-2 of
+// the result was lost. bf16 patterns 128 + q need a shift for every pair of codes.)
 //
 // The bound is HBM: a weight is read once and used for at most 8 tokens (0.5 byte per 16 operations), so
 // what matters is bytes in flight and few instructions per weight. A one-token product cannot fill the
@@ -58,14 +59,14 @@ constexpr int MAX_SLICES = 8;                          // portable cluster size
 
 // Shared memory for chunks of `xg` groups of `mp` tokens (mp = 1, 2, 4 or 8).
 __host__ __device__ constexpr int smem_bytes(int xg, int mp) {
-  return PART_BYTES + xg * 256 * mp + (xg * PARAM_LD + 1) / 2 * 16 + xg * TOKENS * 12;
+  return PART_BYTES + xg * 256 * mp + (xg * PARAM_LD + 1) / 2 * 16 + xg * TOKENS * 8;
 }
 // The most groups that fit: what precedes a chunk's first group (its X, steps and zero points on their way, the sums of X)
 // leaves the loads of the codes with the three groups ahead, so few, long and equal chunks
 // (17 groups of 5 tokens as one chunk of 20 and not 16 + 1: 20.6 to 19.7 us). With 74 KB per CTA the L1 that remains holds too few
 // loads: 28672 -> 8192 for 8 tokens 46 to 55 us.
 __host__ __device__ constexpr int chunk_groups(int mp) {
-  return (CHUNK_BYTES - PART_BYTES) / (256 * mp + 8 * PARAM_LD + TOKENS * 12) / DEPTH * DEPTH;
+  return (CHUNK_BYTES - PART_BYTES) / (256 * mp + 8 * PARAM_LD + TOKENS * 8) / DEPTH * DEPTH;
 }
 constexpr int SMEM_MAX = CHUNK_BYTES;
 static_assert(smem_bytes(chunk_groups(1), 1) <= SMEM_MAX && smem_bytes(chunk_groups(2), 2) <= SMEM_MAX &&
@@ -125,23 +126,19 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// c = a b + (c0, c1, c0, c1)
-__device__ __forceinline__ void mma16816_from(float (&c)[4], float c0, float c1, uint32_t a0, uint32_t a1, uint32_t a2,
-                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+// c = a b
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %10, %11};"
+      "{%10, %10, %10, %10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-// (w & mask) | magic in one instruction (from two operators the compiler made two).
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
-  return d;
-}
-// Codes 0 and 4 of a word as fp16 (1024 + q); codes 1 and 5 as 64 + q. The other four: the same of w >> 8.
-__device__ __forceinline__ uint32_t code_even(uint32_t w) { return and_or(w, 0x000F000Fu, 0x64006400u); }
-__device__ __forceinline__ uint32_t code_odd(uint32_t w) { return and_or(w, 0x00F000F0u, 0x54005400u); }
+// Codes 0 and 4 of a word as fp16 numbers q 2^-24, codes 1 and 5 as q 2^-20. The other four: the same of w >> 8.
+__device__ __forceinline__ uint32_t code_even(uint32_t w) { return w & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t code_odd(uint32_t w) { return w & 0x00F000F0u; }
+// Minus one in the same units.
+constexpr uint32_t MINUS_EVEN = 0x80018001u, MINUS_ODD = 0x80108010u;
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
@@ -155,7 +152,7 @@ template <bool GATED>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint4 zero;      // X of tokens past mp
-  __shared__ unsigned apart;  // bit m: token m holds an infinity or a NaN in this slice
+  __shared__ unsigned apart;  // bit m: token m is summed term by term in this slice
   if (threadIdx.x == 0) {
     zero = make_uint4(0u, 0u, 0u, 0u);
     apart = 0u;
@@ -193,8 +190,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
   float* part = reinterpret_cast<float*>(smem);
   uint8_t* xs = smem + PART_BYTES;                                         // [group][word][token][t4] 16 bytes
   float2* param = reinterpret_cast<float2*>(xs + (p.xg * 256 << p.mp_log2));  // [group][PARAM_LD]: step, zero point
-  float2* sx = param + (p.xg * PARAM_LD + 1) / 2 * 2;  // [group][TOKENS]: -(constants' sum), -(sum of xs)
-  float* back = reinterpret_cast<float*>(sx + p.xg * TOKENS);    // [group][TOKENS]: 1 / c
+  float2* sx = param + (p.xg * PARAM_LD + 1) / 2 * 2;  // [group][TOKENS]: -(sum of xs) 2^-24, 2^24 / c
 
   const uint32_t* codes = p.codes + e * p.O * (p.K / 8) + g_begin * 16;
   const uint32_t* code[4];  // the lane's pieces of its rows g8, g8 + 8, g8 + 16, g8 + 24
@@ -210,7 +206,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
   };
 
   // X of the tokens and of groups gc..gc+ng-1 as fp16, scaled and permuted so that one 16-byte piece (in-features
-  // 8w..8w+7) holds the pairs (0, 4), (1, 5), (2, 6), (3, 7). The 16 threads of a token's group are neighbours.
+  // 8w..8w+7) holds the pairs (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16. The 16 threads of a token's group are neighbours.
   auto stage_x = [&](int gc, int ng) {
     const int per_token = ng * 16;
     constexpr int AT_ONCE = 4;  // loads in flight per thread
@@ -236,21 +232,21 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
         uint32_t most = max(max(exponent_max(v[k].x), exponent_max(v[k].y)), max(exponent_max(v[k].z), exponent_max(v[k].w)));
 #pragma unroll
         for (int d = 1; d < 16; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-        // c = 2^(14 - exponent), kept below 2^127 so that 1 / c is a normal number
+        // c = 2^(14 - exponent), below 2^127; 2^24 / c is a normal number up to an exponent of 117
         const uint32_t field = min(268u - (most >> 7), 253u);
-        const float scale = __uint_as_float(field << 23);
+        const float scale = __uint_as_float(field << 23), odd = __uint_as_float((field - 4u) << 23);
         __half2 h[4];
         h[0] = __floats2half2_rn(bf16_lo(v[k].x) * scale, bf16_lo(v[k].z) * scale);
-        h[1] = __floats2half2_rn(bf16_hi(v[k].x) * scale, bf16_hi(v[k].z) * scale);
+        h[1] = __floats2half2_rn(bf16_hi(v[k].x) * odd, bf16_hi(v[k].z) * odd);
         h[2] = __floats2half2_rn(bf16_lo(v[k].y) * scale, bf16_lo(v[k].w) * scale);
-        h[3] = __floats2half2_rn(bf16_hi(v[k].y) * scale, bf16_hi(v[k].w) * scale);
+        h[3] = __floats2half2_rn(bf16_hi(v[k].y) * odd, bf16_hi(v[k].w) * odd);
         if (to[k] >= 0) {
           const int mk = to[k] >> 16, ck = to[k] & 0xFFFF;
           const int grp = ck >> 4, t = (ck >> 2) & 3, word = ck & 3;
           *reinterpret_cast<uint4*>(xs + (((grp * 4 + word) * mp + mk) * 4 + t) * 16) = *reinterpret_cast<const uint4*>(h);
           if ((ck & 15) == 0) {
-            back[grp * TOKENS + mk] = __uint_as_float((254u - field) << 23);
-            if (most == 0x7F80u) atomicOr(&apart, 1u << mk);
+            sx[grp * TOKENS + mk].y = __uint_as_float(min(278u - field, 254u) << 23);
+            if (field < 24u) atomicOr(&apart, 1u << mk);  // 2^118 and more, infinities, NaN
           }
         }
       }
@@ -265,20 +261,20 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = lds128(at + k * x_word);
   };
-  // Per group and token what the constants add (rows 0-7 of the tile: 1024 or 64 per in-feature) and the sum of xs (rows
-  // 8-15), both with the sign that takes them off.
+  // Minus the sum of xs per group and token.
   auto sum_x = [&](int ng) {
     for (int gx = warp; gx < ng; gx += WARPS) {
       load_x(x_lane + gx * x_group);
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float s[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        mma16816(s, 0xE400E400u, 0xBC00BC00u, 0xD400D400u, 0xBC00BC00u, x[k].x, x[k].y);
-        mma16816(s, 0xE400E400u, 0xBC00BC00u, 0xD400D400u, 0xBC00BC00u, x[k].z, x[k].w);
+        if (k == 0) mma16816_first(s, MINUS_EVEN, MINUS_EVEN, MINUS_ODD, MINUS_ODD, x[k].x, x[k].y);
+        else mma16816(s, MINUS_EVEN, MINUS_EVEN, MINUS_ODD, MINUS_ODD, x[k].x, x[k].y);
+        mma16816(s, MINUS_EVEN, MINUS_EVEN, MINUS_ODD, MINUS_ODD, x[k].z, x[k].w);
       }
-      if (g8 == 0) {
-        sx[gx * TOKENS + 2 * t4] = make_float2(s[0], s[2]);
-        sx[gx * TOKENS + 2 * t4 + 1] = make_float2(s[1], s[3]);
+      if (g8 == 0) {  // the rows of the result are all the same
+        sx[gx * TOKENS + 2 * t4].x = s[0];
+        sx[gx * TOKENS + 2 * t4 + 1].x = s[1];
       }
     }
   };
@@ -320,7 +316,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
     __syncthreads();
     const float2* pa = param + warp * 32 + g8;
     const float2* sa = sx + 2 * t4;
-    const float* ba = back + 2 * t4;
     uint32_t xa = x_lane;
     for (int g0 = 0; g0 < chunk; g0 += DEPTH) {
 #pragma unroll
@@ -329,7 +324,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
         load((d + DEPTH - 1) % DEPTH, d + DEPTH - 1);
         load_x(xa);
         const float4 sums = *reinterpret_cast<const float4*>(sa);  // two tokens
-        const float2 bk = *reinterpret_cast<const float2*>(ba);
         float s[2][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -338,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
             const uint32_t lo = word_of(w[d][2 * i], k), hi = word_of(w[d][2 * i + 1], k);
             const uint32_t l8 = lo >> 8, h8 = hi >> 8;
             if (k == 0)
-              mma16816_from(s[i], sums.x, sums.z, code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
+              mma16816_first(s[i], code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
             else
               mma16816(s[i], code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
             mma16816(s[i], code_even(l8), code_even(h8), code_odd(l8), code_odd(h8), x[k].z, x[k].w);
@@ -346,14 +340,13 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float2 lo = pa[16 * i], hi = pa[16 * i + 8];
-          acc[i][0] = fmaf(lo.x * bk.x, fmaf(lo.y, sums.y, s[i][0]), acc[i][0]);
-          acc[i][1] = fmaf(lo.x * bk.y, fmaf(lo.y, sums.w, s[i][1]), acc[i][1]);
-          acc[i][2] = fmaf(hi.x * bk.x, fmaf(hi.y, sums.y, s[i][2]), acc[i][2]);
-          acc[i][3] = fmaf(hi.x * bk.y, fmaf(hi.y, sums.w, s[i][3]), acc[i][3]);
+          acc[i][0] = fmaf(lo.x, fmaf(lo.y, sums.x, s[i][0]) * sums.y, acc[i][0]);
+          acc[i][1] = fmaf(lo.x, fmaf(lo.y, sums.z, s[i][1]) * sums.w, acc[i][1]);
+          acc[i][2] = fmaf(hi.x, fmaf(hi.y, sums.x, s[i][2]) * sums.y, acc[i][2]);
+          acc[i][3] = fmaf(hi.x, fmaf(hi.y, sums.z, s[i][3]) * sums.w, acc[i][3]);
         }
         pa += PARAM_LD;
         sa += TOKENS;
-        ba += TOKENS;
         xa += x_group;
       }
 #pragma unroll
@@ -371,9 +364,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
     mine[(2 * t4) * PART_LD + 8] = acc[i][2];
     mine[(2 * t4 + 1) * PART_LD + 8] = acc[i][3];
   }
-  // What the group sums cannot give, since they take z sum x off sum q x: tokens with an infinity or a NaN again, term by
-  // term from the weights as fp32 numbers, so that each output is the infinity or the NaN of the definition (as in the
-  // experts' grouped kernel). A column of the MMA is a token, so the others have not been touched.
+  // What the group sums cannot give, since they take z sum x off sum q x: tokens with an infinity or a NaN again (or with a
+  // value of 2^118 and more, whose 2^24 / c is no number), term by term from the weights as fp32 numbers, so that each
+  // output is the infinity or the NaN of the definition (as in the experts' grouped kernel). A column of the MMA is a token,
+  // so the others have not been touched.
   const unsigned tokens_apart = apart;
   if (tokens_apart != 0u) {
     __syncwarp();
