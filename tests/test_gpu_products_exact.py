@@ -105,3 +105,24 @@ def test_few_tokens_of_any_size():
     assert torch.equal(got[[0, 2, 3]], base[[0, 2, 3]])
     ref, err = bounds.term_by_term(X2[1:2], *W)
     plain.assert_within(got[1:2], ref, err)
+
+
+@pytest.mark.parametrize("rows", [1, 8, 12])
+def test_gate_over_the_whole_range(rows):
+    """silu(a) b for a from -104 to 110, where exp(-a) passes the largest float and silu becomes subnormal, and b from 2^-20
+    to 2^100: 2 units each of the exponential and the quotient, 3 roundings besides, and where that is subnormal its spacing of
+    2^-149, times a b."""
+    a = torch.linspace(-104, 110, 1500)
+    b = 2.0 ** torch.tensor([-20.0, 0, 60, 100]).repeat(375)
+    K, I = 128, 1500
+    codes = torch.ones(1, 2 * I, K // 8, dtype=torch.int32)  # in-feature 0 has the code 1
+    steps = torch.cat((a, b)).view(1, 2 * I, 1)
+    zeros = torch.zeros_like(steps)
+    X = torch.zeros(rows, K, dtype=torch.bfloat16)
+    X[:, 0] = 1.0
+    got = awq.w4a16_experts(X.cuda(), offsets_of([rows]).cuda(), codes.cuda(), steps.cuda(), zeros.cuda(), gated=True)
+    ref = a.double() * torch.sigmoid(a.double()) * b.double()
+    err = 6 * 2.0 ** -23 * ref.abs() + 2.0 ** -149 * (a.double() * b.double()).abs()
+    for row in got:
+        plain.assert_within(row[None], ref[None], err[None])
+    assert int(((ref.abs() > 1e-30) & (a < -88.8)).sum()) > 20  # the case shows it
