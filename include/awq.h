@@ -90,6 +90,10 @@ AWQ_API int awq_version(void);
  * 2e9. Applies to calls enqueued after it. Values below 1e6 are raised to 1e6. */
 AWQ_API void awq_set_wait_limit_ns(uint64_t ns);
 
+/* Test hook, like AWQ_FLAG_INJECT_STALL: in later calls of awq_w4a16_experts the MMAs of tile `tile` (tiles counted over the
+ * experts of more than 8 rows) wait for a barrier that nobody signals. -1, the default: nowhere. */
+AWQ_API void awq_set_experts_stall(int tile);
+
 /* ---------------------------------------------------------------------------------------------------
  * (1) Activation statistic.  act_mean[k] = RN32(RN64(S_k / N)) with S_k = sum_i |X[i,k]| accumulated
  * in fp64 in a fixed order: rows in consecutive chunks of 256, inside a chunk one row at a time in

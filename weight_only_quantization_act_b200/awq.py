@@ -41,6 +41,7 @@ SIGNATURES = {
     "awq_last_error": (ctypes.c_char_p, []),
     "awq_version": (_I, []),
     "awq_set_wait_limit_ns": (None, [ctypes.c_uint64]),
+    "awq_set_experts_stall": (None, [_I]),
     "awq_set_profile_events": (None, [_P, _P]),
     "awq_act_stats_workspace_size": (_SZ, [_I64, _I64]),
     "awq_act_stats": (_I, [_P, _I64, _I64, _I64, _P, _SZ, _P, _P]),
@@ -167,6 +168,11 @@ def _workspace(nbytes: int, device, workspace: torch.Tensor | None) -> torch.Ten
 
 def set_wait_limit_ns(ns: int) -> None:
     load_library().awq_set_wait_limit_ns(int(ns))
+
+
+def set_experts_stall(tile: int) -> None:
+    """Test hook: later calls of w4a16_experts wait at this tile for what nobody signals (-1: nowhere)."""
+    load_library().awq_set_experts_stall(int(tile))
 
 
 def set_profile_events(before, after) -> None:

@@ -26,6 +26,7 @@ thread_local char g_err[512] = "";
 thread_local cudaEvent_t g_prof_before = nullptr;
 thread_local cudaEvent_t g_prof_after = nullptr;
 std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
+std::atomic<int> g_experts_stall{-1};
 
 awq_status fail(awq_status s, const char* fmt, ...) {
   va_list ap;
@@ -406,6 +407,8 @@ void awq_set_profile_events(void* before_loss_gemm, void* after_loss_gemm) {
 }
 
 void awq_set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns.store(ns < 1000000ull ? 1000000ull : ns); }
+
+void awq_set_experts_stall(int tile) { g_experts_stall.store(tile); }
 
 size_t awq_act_stats_workspace_size(int64_t N, int64_t K) {
   if (N < 1 || K < 1) return 0;

@@ -344,6 +344,7 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   q.pair_params = q.G % 2 == 0 && ((reinterpret_cast<uintptr_t>(steps) | reinterpret_cast<uintptr_t>(zeros)) & 7u) == 0;
   q.status = static_cast<awq::DeviceStatus*>(workspace);
   q.limit_ns = g_wait_limit_ns.load();
+  q.stall_tile = g_experts_stall.load();
   // The two kernels write different rows, so the second starts as the first one's SMs fall free (an empty grouped kernel
   // costs 8 us by itself).
   cudaLaunchConfig_t cfg = {};

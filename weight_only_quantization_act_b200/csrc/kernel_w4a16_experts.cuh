@@ -103,6 +103,7 @@ struct Params {
   int E;
   int n_bands;             // tiles along the weight rows
   int pair_params;         // steps and zero points of two groups can be copied as 8 bytes
+  int stall_tile;          // test hook: at this tile the MMAs wait for what nobody signals (-1: nowhere)
   DeviceStatus* status;
   uint64_t limit_ns;
 };
@@ -189,27 +190,57 @@ __device__ __forceinline__ uint32_t unpack_pair_any(uint32_t byte, float z) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Bounded wait. One that gives up, after the limit or because another has, returns like any other: the roles run on to the
-// end of their tile, where they look at the status, so that a wait costs its poll and one branch in the loops (a result
-// to carry and test cost the scaling warps a third of their instructions). The status and the clock are looked at after 64
-// polls; a time that the hardware may suspend the thread for, given with the poll, cost 2 to 4 % by waking it late.
-__device__ __forceinline__ void wait_slow(uint32_t bar, uint32_t parity, DeviceStatus* st, uint64_t limit, unsigned where) {
+// Bounded waits. One that gives up, after the limit or because another has, says so, and from there on its role arrives on no
+// barrier and issues no copy, MMA or store that only a completed wait allows: nothing downstream takes an unfinished group
+// for a finished one, and no more than the rings hold is in flight. The status and the clock are looked at after 64
+// polls, so a wait that is met costs its poll and one branch; a time that the hardware may suspend the thread for, given
+// with the poll, cost 2 to 4 % by waking it late.
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, DeviceStatus* st, uint64_t limit, unsigned where) {
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return;
+    if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
-    if (status_code(st) != 0u) return;
+    if (status_code(st) != 0u) return false;
     if (global_timer_ns() - t0 > limit) {
       raise_timeout(st, where);
-      return;
+      return false;
     }
   }
+  return true;
 }
-__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, const Params& p, unsigned where) {
-  if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, p.status, p.limit_ns, where);
+// For one thread. Where all lanes of a warp poll, what lane 0 has seen counts: after a __syncwarp the phase is complete for the
+// others too, also for one that has given up.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Params& p, unsigned where) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, p.status, p.limit_ns, where);
 }
+// For a whole warp, which gets one answer: lane 0 decides to give up. (The scaling warps vote once per tile, since nothing but
+// their arrivals counts until then: with a vote per wait 600 rows to 8 experts of 14336 -> 4096 took 169 us, not 156.)
+__device__ __forceinline__ bool wait_warp_slow(uint32_t bar, uint32_t parity, DeviceStatus* st, uint64_t limit, unsigned where) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (i < 64) continue;
+    bool give_up = false;
+    if ((threadIdx.x & 31) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (i == 64) t0 = now;
+      give_up = status_code(st) != 0u;
+      if (!give_up && now - t0 > limit) {
+        raise_timeout(st, where);
+        give_up = true;
+      }
+    }
+    if (__any_sync(0xffffffffu, give_up)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Params& p, unsigned where) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_warp_slow(bar, parity, p.status, p.limit_ns, where);
+}
+// The status as lane 0 finds it, for the whole warp.
+__device__ __forceinline__ bool warp_ok(const DeviceStatus* st) { return __shfl_sync(0xffffffffu, status_code(st), 0) == 0u; }
 
 template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
@@ -217,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                          const __grid_constant__ CUtensorMap tmX3, const __grid_constant__ CUtensorMap tmC, Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * STAGES + 2 * CSTAGES + 1];
+  __shared__ __align__(8) uint64_t bars[2 * STAGES + 2 * CSTAGES + 2];
   __shared__ uint32_t tmem_slot;
   __shared__ int widest;  // tokens of the call's widest tile
   int* first_row = reinterpret_cast<int*>(smem + STAGES * X_BYTES + CSTAGES * CSTAGE_BYTES);  // [E + 1]
@@ -234,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto cfull_bar = [&](int c) { return bar0 + 8u * (2 * STAGES + c); };             // codes and parameters landed
   auto cempty_bar = [&](int c) { return bar0 + 8u * (2 * STAGES + CSTAGES + c); };  // and read
   const uint32_t full0 = map_to_rank(bar0, 0);  // the even CTA's full_bar(0)
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * CSTAGES);
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * CSTAGES), never_bar = drain_bar + 8u;
   const uint32_t smem_base = smem_u32(smem);
   auto x_tile = [&](uint32_t i) { return smem_base + (i % STAGES) * X_BYTES; };
   auto c_tile = [&](int c) { return smem_base + static_cast<uint32_t>(STAGES * X_BYTES + c * CSTAGE_BYTES); };
@@ -249,6 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(cempty_bar(c), DQ_WARPS + EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(never_bar, 1);
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -321,7 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------------------------------ TMA (token rows)
       uint32_t i = 0;
       const uint64_t pol = policy_evict_normal();
-      for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
+      bool ok = true;
+      for (int t = pair; ok && t < num_tiles && status_code(st) == 0u; t += n_pairs) {
         const Tile tile = tile_at(t);
         const int half = static_cast<int>(tile.n() / 2);
         const int boxes = (half + X_BOX - 1) / X_BOX;
@@ -329,7 +362,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t bytes = static_cast<uint32_t>(boxes * X_BOX * BK * 2 * 2 * 2);  // both halves, both CTAs
         const int32_t row = tile.row0 + static_cast<int32_t>(rank) * half;
         for (int g = 0; g < num_groups; ++g, ++i) {
-          if (i >= STAGES) wait(done_bar(i), parity(i - STAGES), p, kSiteTmaEmpty);
+          ok = i < STAGES || wait(done_bar(i), parity(i - STAGES), p, kSiteTmaEmpty);
+          if (!ok) break;
           const uint32_t fb = full0 + 8u * (i % STAGES);
           if (rank == 0) mbar_arrive_expect_tx(full_bar(i), bytes);
           tma_load_2d_pair_hint(x_tile(i), map, g * 2 * BK, row, fb, pol);
@@ -340,10 +374,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------------------------------ MMA (even CTA)
       uint32_t i = 0, buf = 0;
       const uint64_t desc0 = smem_desc_sw128(x_tile(0));
-      for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
+      bool ok = true;
+      for (int t = pair; ok && t < num_tiles && status_code(st) == 0u; t += n_pairs) {
         const uint32_t idesc = idesc_bf16_f32(2 * HALF, tile_at(t).n());
-        for (int g = 0; g < num_groups; ++g, ++i) {
-          wait(full_bar(i), parity(i), p, kSiteMmaFull);
+        if (t == p.stall_tile) ok = wait(never_bar, 0u, p, kSiteMmaInjected);
+        for (int g = 0; ok && g < num_groups; ++g, ++i) {
+          ok = wait(full_bar(i), parity(i), p, kSiteMmaFull);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem_base + buf * buf_cols, a = d + acc_cols;
           if (++buf == depth) buf = 0;
@@ -367,11 +404,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------------------------------ TMA (codes)
       int slot = 0;
       uint32_t phase = 0;
-      for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
+      bool ok = true;
+      for (int t = pair; ok && t < num_tiles && status_code(st) == 0u; t += n_pairs) {
         const Tile tile = tile_at(t);
         const int32_t w0 = tile.e * static_cast<int32_t>(p.O);
         for (int j = 0; j < num_slots; ++j) {
-          wait(cempty_bar(slot), phase ^ 1u, p, kSiteTmaProduced);
+          ok = wait(cempty_bar(slot), phase ^ 1u, p, kSiteTmaProduced);
+          if (!ok) break;
           mbar_arrive_expect_tx(cfull_bar(slot), C_BYTES);
           if (GATED) {
             const int32_t out0 = tile.band * HALF + static_cast<int32_t>(rank) * (HALF / 2);
@@ -394,7 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------------------------------ steps and zero points
       int slot = 0;
       uint32_t phase = 0;
-      for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
+      bool ok = true;
+      for (int t = pair; ok && t < num_tiles && warp_ok(st); t += n_pairs) {
         const Tile tile = tile_at(t);
         int64_t row[4];
 #pragma unroll
@@ -409,8 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           row[i] = (static_cast<int64_t>(tile.e) * p.O + o) * p.G;
         }
         for (int j = 0; j < num_slots; ++j) {
-          wait(cempty_bar(slot), phase ^ 1u, p, kSiteTmaProduced);
-          __syncwarp();
+          ok = wait_warp(cempty_bar(slot), phase ^ 1u, p, kSiteTmaProduced);
+          if (!ok) break;
           const int g = 2 * j;
           const uint32_t dst = c_tile(slot) + C_BYTES + static_cast<uint32_t>(lane * 8);
 #pragma unroll
@@ -452,13 +492,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t zp = static_cast<uint32_t>(C_BYTES + P_BYTES + set * 4) - static_cast<uint32_t>(r * 120);  // from `line`
     int slot = 0;
     uint32_t phase = 0, i = 0;
-    for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
+    bool ok = true;
+    for (int t = pair; ok && t < num_tiles && warp_ok(st); t += n_pairs) {
       uint32_t buf = (i + static_cast<uint32_t>(set)) % depth;
       uint32_t n = i + static_cast<uint32_t>(set);
       i += static_cast<uint32_t>(num_groups);
 #pragma unroll 1
       for (int j = 0; j < num_slots; ++j) {
-        wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
+        ok = wait_warp(cfull_bar(slot), phase, p, kSiteTmaEmpty);
+        if (!ok) break;
         if (n != i) {  // the last slot may hold one group
           const uint32_t line = first + static_cast<uint32_t>(slot * CSTAGE_BYTES);
           float z;
@@ -477,8 +519,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int c = 0; c < 8; ++c) unpack_word(w[c], zb, o + 4 * c);
           }
           const uint4 w0 = few::lds128(line + at2), w1 = few::lds128(line + at3);
-          if (n >= depth) wait(done_bar(n - depth), parity(n - depth), p, kSiteTmaProduced);
-          __syncwarp();
+          ok = n < depth || wait_warp(done_bar(n - depth), parity(n - depth), p, kSiteTmaProduced);
+          if (!ok) break;
           tc_fence_after();  // the MMAs that read the buffer come before the stores below
           tmem_st32(to, o);
           {
@@ -523,9 +565,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t c_first = c_tile(0) + C_BYTES + static_cast<uint32_t>(r * 8);
     const uint32_t ta0 = tmem_base + static_cast<uint32_t>(half * BLOCK) + (static_cast<uint32_t>(quarter * 32) << 16);
     uint32_t phase = 0, i = 0, buf = 0, ct = c_first, ta = ta0;
+    int who = lane;  // the lane with 0 here arrives for the warp; -1 where it has given up
     if (lane == 0)  // every accumulator is free
       for (uint32_t d = 0; d < depth; ++d) mbar_arrive_pair(map_to_rank(full_bar(d), 0));
-    for (int t = pair; t < num_tiles && status_code(st) == 0u; t += n_pairs) {
+    for (int t = pair; t < num_tiles && warp_ok(st); t += n_pairs) {
       const Tile tile = tile_at(t);
       const int blocks = (tile.tokens + BLOCK - 1) / BLOCK;
       const int mine = (blocks - half + 1) / 2;  // this warp's blocks: half, half + 2, ...
@@ -542,10 +585,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll (N > 1 ? 1 : 2)
         for (int g = 0; g < num_groups; ++g, ++i) {
           if ((g & 1) == 0) {
-            wait(cfull_bar(slot), phase, p, kSiteTmaEmpty);
+            if (!wait(cfull_bar(slot), phase, p, kSiteTmaEmpty)) who = -1;
             steps = few::lds64f(ct);
             __syncwarp();
-            if (lane == 0) mbar_arrive(cempty_bar(slot));
+            if (who == 0) mbar_arrive(cempty_bar(slot));
             ct += CSTAGE_BYTES;
             if (++slot == CSTAGES) {
               slot = 0;
@@ -555,7 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           const uint32_t s64 = __float_as_uint(((g & 1) ? steps.y : steps.x) * 64.0f);
           const uint64_t ss = f32x2_pack(s64, s64);
-          wait(done_bar(i), parity(i), p, kSiteEpiAccFull);
+          if (!wait(done_bar(i), parity(i), p, kSiteEpiAccFull)) who = -1;
           __syncwarp();
           tc_fence_after();
 #pragma unroll
@@ -567,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_pair(full0 + 8u * ((i + depth) % STAGES));  // the group that overwrites it
+          if (who == 0) mbar_arrive_pair(full0 + 8u * ((i + depth) % STAGES));  // the group that overwrites it
           ta += buf_cols;
           if (++buf == depth) {
             buf = 0;
@@ -578,7 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (mine >= 3) scale_groups(std::integral_constant<int, 3>{});
       else if (mine == 2) scale_groups(std::integral_constant<int, 2>{});
       else scale_groups(std::integral_constant<int, 1>{});
-      if (status_code(st) != 0u) break;  // nothing of an unfinished tile is stored
+      if (!__any_sync(0xffffffffu, who == 0)) break;  // nothing of an unfinished tile is stored
 
       int64_t o, n_out;
       if (GATED) {
@@ -621,9 +664,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
   }
 
-  if (status_code(st) != 0u) {  // after a timeout: give the copies in flight time to land
+  // After a timeout: time for the copies in flight to land. A role that gave up has seen the status set, so it waits here, and
+  // the pair ends together.
+  if (!warp_ok(st)) {
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 50000ull) __nanosleep(1000);
+    __syncwarp();
   }
   tc_fence_before();
   cluster_sync();
