@@ -73,3 +73,42 @@ def test_a_pair_with_more_tiles_ends(short_limit, rows, tile, gated):
     assert bool(left.any()) and bool((left | (out == clean)).all())
     ws.zero_()
     assert torch.equal(awq.w4a16_experts(X, offsets, *W, gated=gated, workspace=ws), clean) and status(ws) == 0
+
+
+def test_status_from_python():
+    """A status word set from the host: reported, the rows left alone, and right again once the workspace is zeroed; through the
+    block too, on the device of the workspace and on another stream."""
+    counts, K, O = [12, 3], 256, 200
+    _, W = expert_weights(2, O, K, 84)
+    X, offsets = normal((15, K), 85).cuda(), offsets_of(counts).cuda()
+    ws = awq.w4a16_experts_workspace(W[0], 15)
+    clean = awq.w4a16_experts(X, offsets, *W, workspace=ws)
+    assert awq.w4a16_status(ws) == 0
+    ws[0] = 5
+    out = torch.full_like(clean, 7.0)
+    awq.w4a16_experts(X, offsets, *W, out=out, workspace=ws)
+    assert awq.w4a16_status(ws) == 5 and awq.STATUS_NAMES[5] == "AWQ_ERR_TIMEOUT"
+    torch.cuda.synchronize()
+    assert awq.w4a16_status(ws, stream=torch.cuda.Stream()) == 5
+    assert bool((out[:12] == 7.0).all()) and torch.equal(out[12:], clean[12:])
+    ws.zero_()
+    awq.w4a16_experts(X, offsets, *W, out=out, workspace=ws)
+    assert awq.w4a16_status(ws) == 0 and torch.equal(out, clean)
+
+
+def test_status_of_a_block(short_limit):
+    E, K, I, T = 2, 256, 128, 40
+    _, gate_up = expert_weights(E, 2 * I, K, 86)
+    _, down = expert_weights(E, K, I, 87)
+    X, ids = normal((T, K), 88).cuda(), (torch.arange(T)[:, None] % E).cuda()
+    weights = torch.ones(T, 1).cuda()
+    ws = (awq.w4a16_experts_workspace(gate_up[0], T), awq.w4a16_experts_workspace(down[0], T))
+    clean = awq.w4a16_moe(X, ids, weights, gate_up, down, workspaces=ws)
+    assert [awq.w4a16_status(w) for w in ws] == [0, 0]
+    awq.set_experts_stall(0)
+    awq.w4a16_moe(X, ids, weights, gate_up, down, workspaces=ws)
+    assert [awq.w4a16_status(w) for w in ws] == [5, 5]
+    awq.set_experts_stall(-1)
+    for w in ws:
+        w.zero_()
+    assert torch.equal(awq.w4a16_moe(X, ids, weights, gate_up, down, workspaces=ws), clean)

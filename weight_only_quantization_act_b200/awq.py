@@ -675,12 +675,27 @@ def w4a16_experts_workspace(codes: torch.Tensor, rows: int) -> torch.Tensor:
 
 
 @_on_stream
+def w4a16_status(workspace: torch.Tensor, *, stream=None) -> int:
+    """Synchronise and return the device status of the calls of w4a16_experts or w4a16_gemm on this workspace (0 = ok, 5 = a
+    device wait gave up; STATUS_NAMES). After a timeout zero the workspace before its next use."""
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
+        raise TypeError("workspace must be a CUDA tensor")
+    _on_device("workspace", workspace, workspace.device)
+    return load_library().awq_search_status(workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                            _current_stream())
+
+
+@_on_stream
 def w4a16_experts(Xs: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, zeros: torch.Tensor,
                   gated: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                   *, stream=None) -> torch.Tensor:
     """Products of sorted rows with their experts' packed weights: Y[r] = Xs[r] deq(W_e)^T for offsets[e] <= r <
     offsets[e + 1] (codes [E, O, K/8], steps and zeros [E, O, K/128]); ``gated`` as in w4a16_gemv. Rows behind the last
-    routed one are not written."""
+    routed one are not written.
+
+    A device wait that gives up (set_wait_limit_ns) leaves rows of experts with more than 8 rows as they were and its status in the
+    workspace, where w4a16_status finds it; until the workspace is zeroed, later calls on it leave such rows alone too.
+    Without a workspace of the caller's a timeout is not reported."""
     lib = load_library()
     Xs = _rows("Xs", Xs)
     R, K = Xs.shape
@@ -702,7 +717,8 @@ def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up
               workspaces=(None, None), out: torch.Tensor | None = None, *, stream=None) -> torch.Tensor:
     """A feed-forward block of quantized experts: tokens X [T, K] sorted by their picks ids [T, k], divided by each
     expert's scales, through silu(gate) * up and the down projection of their experts, and back, weighted. gate_up and
-    down are (codes, steps, zeros) of all experts, as quantize_experts gives them."""
+    down are (codes, steps, zeros) of all experts, as quantize_experts gives them. workspaces: one of w4a16_experts_workspace
+    for each of the two products, whose w4a16_status then tells of a device timeout (without them it is not reported)."""
     sort = expert_sort(ids, gate_up[0].shape[0])
     Xs = expert_gather(X, sort, scales=scales)
     H = w4a16_experts(Xs, sort.offsets, *gate_up, gated=True, workspace=workspaces[0])
