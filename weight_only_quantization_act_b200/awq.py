@@ -714,14 +714,20 @@ def w4a16_experts(Xs: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor, 
 
 @_on_stream
 def w4a16_moe(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up, down, scales: torch.Tensor | None = None,
-              workspaces=(None, None), out: torch.Tensor | None = None, *, stream=None) -> torch.Tensor:
+              workspaces=(None, None), out: torch.Tensor | None = None, *, down_scales: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
     """A feed-forward block of quantized experts: tokens X [T, K] sorted by their picks ids [T, k], divided by each
     expert's scales, through silu(gate) * up and the down projection of their experts, and back, weighted. gate_up and
-    down are (codes, steps, zeros) of all experts, as quantize_experts gives them. workspaces: one of w4a16_experts_workspace
+    down are (codes, steps, zeros) of all experts, as quantize_experts gives them; scales [E, K] and down_scales [E, I] the
+    scales that it gave with each, None where they are folded into what comes before (the down projection's into the up
+    rows: fold_linear_linear before packing those). workspaces: one of w4a16_experts_workspace
     for each of the two products, whose w4a16_status then tells of a device timeout (without them it is not reported)."""
     sort = expert_sort(ids, gate_up[0].shape[0])
     Xs = expert_gather(X, sort, scales=scales)
     H = w4a16_experts(Xs, sort.offsets, *gate_up, gated=True, workspace=workspaces[0])
+    if down_scales is not None:  # sorted rows stay where they are: each row is its own token
+        rows = torch.arange(H.shape[0], dtype=torch.int32, device=H.device)
+        H = expert_gather(H, ExpertSort(sort.offsets, rows, rows[:, None]), scales=down_scales)
     Ys = w4a16_experts(H, sort.offsets, *down, workspace=workspaces[1])
     return expert_combine(Ys, sort, weights=weights, out=out)
 
