@@ -27,6 +27,13 @@ awq_status check_packed(const void* codes, const float* steps, const float* zero
   return AWQ_OK;
 }
 
+// An array of int32 or float.
+awq_status check_words(const char* name, const void* p) {
+  if (p == nullptr) return fail(AWQ_ERR_INVALID_ARG, "%s must be given", name);
+  if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return fail(AWQ_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
+  return AWQ_OK;
+}
+
 awq_status check_experts(int64_t E) {
   if (E < 1 || E > AWQ_MAX_EXPERTS)
     return fail(AWQ_ERR_INVALID_ARG, "%lld experts: 1 to %d are supported", static_cast<long long>(E), AWQ_MAX_EXPERTS);
@@ -198,7 +205,8 @@ extern "C" awq_status awq_expert_gather(const void* X, int64_t T, int64_t K, int
   AWQ_TRY(check_rows_args(T, top_k, K));
   AWQ_TRY(check_matrix("Xs", Xs, T * top_k, K, ldxs));
   AWQ_TRY(check_experts(E));
-  if (offsets == nullptr || order == nullptr) return fail(AWQ_ERR_INVALID_ARG, "offsets and order must be given");
+  AWQ_TRY(check_words("offsets", offsets));
+  AWQ_TRY(check_words("order", order));
   if (!aligned16(scales)) return fail(AWQ_ERR_INVALID_ARG, "scales is not 16-byte aligned");
   DeviceInfo* d = nullptr;
   AWQ_TRY(device_info(&d));
@@ -247,7 +255,8 @@ extern "C" awq_status awq_expert_gather_backward(const void* dXs, int64_t T, int
   AWQ_TRY(check_rows_args(T, top_k, K));
   AWQ_TRY(check_matrix("dXs", dXs, T * top_k, K, lddxs));
   AWQ_TRY(check_experts(E));
-  if (offsets == nullptr || pos == nullptr) return fail(AWQ_ERR_INVALID_ARG, "offsets and pos must be given");
+  AWQ_TRY(check_words("offsets", offsets));
+  AWQ_TRY(check_words("pos", pos));
   if (!aligned16(scales)) return fail(AWQ_ERR_INVALID_ARG, "scales is not 16-byte aligned");
   return combine(dXs, T, K, lddxs, top_k, pos, nullptr, offsets, E, scales, dX, lddx, stream);
 }
@@ -258,7 +267,8 @@ extern "C" awq_status awq_expert_combine(const void* Ys, int64_t T, int64_t O, i
   AWQ_TRY(check_matrix("Y", Y, T, O, ldy));
   AWQ_TRY(check_rows_args(T, top_k, O));
   AWQ_TRY(check_matrix("Ys", Ys, T * top_k, O, ldys));
-  if (pos == nullptr) return fail(AWQ_ERR_INVALID_ARG, "pos must be given");
+  AWQ_TRY(check_words("pos", pos));
+  if (weights != nullptr) AWQ_TRY(check_words("weights", weights));
   return combine(Ys, T, O, ldys, top_k, pos, weights, nullptr, 0, nullptr, Y, ldy, stream);
 }
 
@@ -269,8 +279,9 @@ extern "C" awq_status awq_expert_combine_backward(const void* dY, int64_t T, int
   AWQ_TRY(check_rows_args(T, top_k, O));
   AWQ_TRY(check_matrix("Ys", Ys, T * top_k, O, ldys));
   AWQ_TRY(check_matrix("dYs", dYs, T * top_k, O, lddys));
-  if (pos == nullptr || weights == nullptr || dweights == nullptr)
-    return fail(AWQ_ERR_INVALID_ARG, "pos, weights and dweights must be given");
+  AWQ_TRY(check_words("pos", pos));
+  AWQ_TRY(check_words("weights", weights));
+  AWQ_TRY(check_words("dweights", dweights));
   DeviceInfo* d = nullptr;
   AWQ_TRY(device_info(&d));
   awq::ex::expert_combine_backward_kernel<<<static_cast<unsigned>(T * top_k), awq::ex::ROW_THREADS, 0,
@@ -293,7 +304,7 @@ extern "C" awq_status awq_w4a16_experts(const void* Xs, int64_t R, int64_t K, in
   AWQ_TRY(check_matrix("Xs", Xs, R, K, ldx));
   AWQ_TRY(check_packed(codes, steps, zeros, O, K, gated));
   AWQ_TRY(check_experts(E));
-  if (offsets == nullptr) return fail(AWQ_ERR_INVALID_ARG, "offsets must be given");
+  AWQ_TRY(check_words("offsets", offsets));
   AWQ_TRY(check_output("Y", Y, R, gated ? O / 2 : O, ldy));
   const size_t need = awq_w4a16_experts_workspace_size(R, E, K, O);
   if (workspace == nullptr || ws_bytes < need)
