@@ -40,3 +40,18 @@ def test_misaligned_words_are_refused(lib):
     for at in (7, 8, 11):  # pos, weights, dweights
         refused(lib.awq_expert_combine_backward, back, at)
     refused(lib.awq_w4a16_experts, (fake, 4, 256, 256, fake, 8, fake, fake, fake, 64, 0, fake, 64, fake, 1 << 30, None), 4)
+
+
+def test_expert_weights_that_do_not_fit_are_refused():
+    """Looked at before anything is launched: an expert without tokens would be packed with scales of X's width."""
+    def bf16(*shape, device="cpu"):
+        return torch.zeros(*shape, dtype=torch.bfloat16, device=device)
+
+    X, ids = bf16(4, 256), torch.zeros(4, 1, dtype=torch.int64)
+    for W in ([bf16(8, 256), bf16(8, 384)], [bf16(8, 384)] * 2, [bf16(8, 128)], [(bf16(8, 256), bf16(8, 512))],
+              [bf16(8, 256), bf16(16, 256)], [bf16(8, 256), (bf16(8, 256), bf16(8, 256))], [], [bf16(8, 256)[None]],
+              [bf16(8, 256, device="meta")]):
+        with pytest.raises(ValueError):
+            awq.quantize_experts(X, ids, W)
+    with pytest.raises(TypeError):  # right shapes, but no GPU tensors
+        awq.quantize_experts(X, ids, [bf16(8, 256), (bf16(4, 256), bf16(4, 256))])

@@ -740,6 +740,17 @@ def quantize_experts(X: torch.Tensor, ids: torch.Tensor, W: Sequence[torch.Tenso
     zeros [E, O, ...], and losses, best_j per expert. An expert without a token is quantized at scales of one (losses NaN,
     best_j 0). Reads the experts' row counts on the host (one synchronisation)."""
     E = len(W)
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise TypeError("X must be a CUDA bfloat16 matrix")
+    rows = set()
+    for e, w in enumerate(W):  # a weight wider than X would be read with scales that are not there
+        parts = [w] if isinstance(w, torch.Tensor) else list(w)
+        for part in parts:
+            if part.dim() != 2 or part.shape[1] != X.shape[1] or part.device != X.device:
+                raise ValueError(f"expert {e}: a weight must be [O, {X.shape[1]}] on {X.device}")
+        rows.add(sum(part.shape[0] for part in parts))
+    if len(rows) != 1:
+        raise ValueError(f"every expert needs as many weight rows as the others, not {sorted(rows)}")
     mats = [stack_weights(w) for w in W]
     sort = expert_sort(ids, E)
     Xs = expert_gather(X, sort)
