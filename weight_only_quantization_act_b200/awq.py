@@ -450,7 +450,8 @@ def w4a16_gemm(X: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, zeros:
 # --------------------------------------------------------------------------------------------- (8)
 def _on_stream(fn):
     """Run an entry point on its first tensor argument's device, and on `stream` where one is given: what it
-    allocates then belongs to that stream, so a workspace is not handed to other work while the stream uses it."""
+    allocates then belongs to that stream, so a workspace is not handed to other work while the stream uses it. The caller's
+    tensors are recorded with the stream, so one that is freed after the call is not reused before the stream has read it."""
 
     @functools.wraps(fn)
     def wrapper(*args, stream=None, **kwargs):
@@ -462,13 +463,26 @@ def _on_stream(fn):
             if on_cuda and stream.device != first.device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
             with torch.cuda.stream(stream):
-                return fn(*args, **kwargs)
+                result = fn(*args, **kwargs)
+            _record(stream, (*args, *kwargs.values()))
+            return result
         if not on_cuda or first.get_device() == torch.cuda.current_device():
             return fn(*args, **kwargs)
         with torch.cuda.device(first.device):
             return fn(*args, **kwargs)
 
     return wrapper
+
+
+def _record(stream, values) -> None:
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            if v.is_cuda:
+                v.record_stream(stream)
+        elif isinstance(v, ExpertSort):
+            _record(stream, (v.offsets, v.order, v.pos))
+        elif isinstance(v, (list, tuple)):
+            _record(stream, v)
 
 
 def _current_stream() -> int:
