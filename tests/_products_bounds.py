@@ -50,3 +50,15 @@ def assert_rounds(got, ref, before=2.0 ** -14):
     off, spacing = differ(got, ref)
     limit = (2 * spacing * before + before ** 2) ** 0.5
     assert off <= limit, (off, limit)
+
+
+def grouped(X, codes, steps, zeros):
+    """The same as `few` for the experts' grouped kernel: per group, (q - z) x summed by 8 MMAs of 16 products and the sum so far,
+    17 addends cut by 2 units of (15 + |z|) A at most, then one rounding per group of the running sum. Where |z| > 240 a
+    weight enters rounded to bf16, off by 2^-8 of its size at most."""
+    A, step, z = _sums(X, steps, zeros)
+    coef = step * (15 + z) * (2 * 17 * 8 + 1 + steps.shape[1])
+    W = plain.dequantized(codes, steps, zeros)
+    err = 2.0 ** -24 * (A @ coef.T)
+    far = (z > 240).repeat_interleave(GROUP, 1)
+    return X.double() @ W.T, err + 2.0 ** -8 * (X.double().abs() @ (W.abs() * far).T)

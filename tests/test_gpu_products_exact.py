@@ -126,3 +126,58 @@ def test_gate_over_the_whole_range(rows):
     for row in got:
         plain.assert_within(row[None], ref[None], err[None])
     assert int(((ref.abs() > 1e-30) & (a < -88.8)).sum()) > 20  # the case shows it
+
+
+# tiles of one and of several widths, two, three and four groups in flight, an odd number of groups
+@pytest.mark.parametrize("rows,K,O", [(9, 384, 130), (16, 384, 264), (48, 640, 257), (96, 640, 300), (97, 1152, 200),
+                                      (200, 1408, 515)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("far", [False, True])
+def test_one_hot_rows_of_experts_are_exact(rows, K, O, gated, far):
+    """A row with a single power of two gets exactly bf16(x RN32((q - z) step)) of each weight: every nibble, the operand's order,
+    the group's step and zero point (up to +-240 they stay exact). Gated, the same two numbers through the gate."""
+    O += O % 2 if gated else 0
+    codes, steps, zeros = plain.packed(O, K, K + rows)
+    if far:
+        zeros = torch.randint(-240, 241, zeros.shape, generator=torch.Generator().manual_seed(K)).float()
+        steps = steps * 0.05
+    deq = plain.dequantized(codes, steps, zeros).float()  # one rounding of the exact product
+    W = tuple(t[None].cuda() for t in (codes, steps, zeros))
+    for first in range(0, K, rows):
+        k = (first + torch.arange(rows)) % K
+        scale = 2.0 ** (torch.arange(rows) % 7 - 3).float()
+        X = torch.zeros(rows, K)
+        X[torch.arange(rows), k] = scale
+        got = awq.w4a16_experts(X.bfloat16().cuda(), offsets_of([rows]).cuda(), *W, gated=gated)
+        want = deq[:, k].T * scale[:, None]
+        if not gated:
+            assert torch.equal(got.cpu(), want.bfloat16()), first
+        else:
+            a, b = want.double().chunk(2, dim=1)
+            ref = a * torch.sigmoid(a) * b
+            plain.assert_within(got, ref, 7 * 2.0 ** -23 * ref.abs())
+
+
+@pytest.mark.parametrize("counts,K,O", [([9, 0, 70, 200], 14336, 300), ([500, 33], 1152, 700), ([12] * 8, 28672, 260)])
+@pytest.mark.parametrize("one_sided", [False, True])
+def test_rows_of_experts_lose_nothing_before_the_rounding(counts, K, O, one_sided):
+    parts = [weights_around_zero(O, K, 170 + e) for e in range(len(counts))]
+    W = tuple(torch.stack([p[i] for p in parts]).cuda() for i in range(3))
+    X = normal((sum(counts), K), 180)
+    X = X.abs() if one_sided else X
+    got = awq.w4a16_experts(X.cuda(), offsets_of(counts).cuda(), *W)
+    row = 0
+    for e, n in enumerate(counts):
+        if n:
+            ref, err = bounds.grouped(X[row:row + n], *parts[e])
+            bounds.assert_rounds(got[row:row + n], ref)
+            plain.assert_within(got[row:row + n], ref, err)
+        row += n
+
+
+def test_rows_of_experts_with_wild_steps_and_zero_points():
+    K, O, rows = 768, 300, 50
+    W = plain.packed(O, K, 190, wild=True)
+    X = normal((rows, K), 191)
+    got = awq.w4a16_experts(X.cuda(), offsets_of([rows]).cuda(), *(t[None].cuda() for t in W))
+    plain.assert_within(got, *bounds.grouped(X, *W))
