@@ -55,3 +55,13 @@ def test_expert_weights_that_do_not_fit_are_refused():
             awq.quantize_experts(X, ids, W)
     with pytest.raises(TypeError):  # right shapes, but no GPU tensors
         awq.quantize_experts(X, ids, [bf16(8, 256), (bf16(4, 256), bf16(4, 256))])
+
+
+def test_no_name_of_the_binding_is_given_twice():
+    """A second definition takes the first one's place for all that is defined after it."""
+    import ast
+    import inspect
+
+    names = [node.name for node in ast.parse(inspect.getsource(awq)).body
+             if isinstance(node, (ast.FunctionDef, ast.ClassDef))]
+    assert len(names) == len(set(names))

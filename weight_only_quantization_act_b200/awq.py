@@ -138,7 +138,7 @@ def _float_vector_out(name: str, out: torch.Tensor, n: int, device) -> torch.Ten
     return out
 
 
-def _on_device(fn):
+def _on_first_device(fn):
     """Run an entry point with its first tensor argument's device current, so that the library launches
     there and the stream passed is that device's current stream."""
 
@@ -196,7 +196,7 @@ def act_stats_workspace_size(N: int, K: int) -> int:
     return load_library().awq_act_stats_workspace_size(N, K)
 
 
-@_on_device
+@_on_first_device
 def act_stats(X: torch.Tensor, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """act_mean[k] = mean_i |X[i,k]| (fixed-order fp64 sum, rounded to fp32)."""
@@ -212,7 +212,7 @@ def act_stats(X: torch.Tensor, out: torch.Tensor | None = None, workspace: torch
     return out
 
 
-@_on_device
+@_on_first_device
 def act_stats_noalloc(X: torch.Tensor, out: torch.Tensor, stream=None) -> torch.Tensor:
     """Same statistic with no workspace, for callers that cannot allocate device memory at call time
     (the scratch is a fixed 16 MiB array inside the library; ceil(N/256)*K <= 2**21). ``out`` must be
@@ -231,7 +231,7 @@ def act_stats_noalloc(X: torch.Tensor, out: torch.Tensor, stream=None) -> torch.
 
 
 # --------------------------------------------------------------------------------------------- (2)
-@_on_device
+@_on_first_device
 def scale_table(act_mean: torch.Tensor, n_grid: int = 20, exact_pow: bool = False, rule: str = "p4",
                 weight_mean: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """float32 [n_grid, K] table of candidate scales; rule "p4" (default), "weight_aware" (needs
@@ -281,7 +281,7 @@ def search_layout(N: int, K: int, O: int, n_grid: int = 20, group: int = 128) ->
     return lay
 
 
-@_on_device
+@_on_first_device
 def search(X: torch.Tensor, W, act_mean: torch.Tensor, n_grid: int = 20, group: int = 128, flags: int = 0,
            workspace: torch.Tensor | None = None, out: SearchResult | None = None, rule: str = "p4",
            quant: str = "int4", stream=None) -> SearchResult:
@@ -328,7 +328,7 @@ def tile_partials(result: SearchResult, N: int, K: int, O: int, n_grid: int = 20
 
 
 # --------------------------------------------------------------------------------------------- (5)
-@_on_device
+@_on_first_device
 def quantize_pack(W: torch.Tensor, scales: torch.Tensor, group: int = 128, flags: int = 0, stream=None):
     """(codes uint32 [O, K/8] as int32 storage, steps float32 [O, K/g], zeros float32 [O, K/g])."""
     lib = load_library()
@@ -343,7 +343,7 @@ def quantize_pack(W: torch.Tensor, scales: torch.Tensor, group: int = 128, flags
     return codes, steps, zeros
 
 
-@_on_device
+@_on_first_device
 def quantize_pack_int8(W: torch.Tensor, scales: torch.Tensor, flags: int = 0, stream=None):
     """(codes int8 [O, K], steps float32 [O]): symmetric INT8, one step per output channel."""
     lib = load_library()
@@ -356,7 +356,7 @@ def quantize_pack_int8(W: torch.Tensor, scales: torch.Tensor, flags: int = 0, st
     return codes, steps
 
 
-@_on_device
+@_on_first_device
 def quantize_layer(X: torch.Tensor, W, n_grid: int = 20, group: int = 128, stream=None):
     """The whole path for one layer: statistic, search, and the packed artefact at the best scales."""
     act = act_stats(X, stream=stream)
@@ -377,7 +377,7 @@ def _as_matrix(t: torch.Tensor) -> torch.Tensor:
     return t.view(1, -1) if t.dim() == 1 else t
 
 
-@_on_device
+@_on_first_device
 def scale_columns(A: torch.Tensor, s: torch.Tensor, divide: bool = False, out: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """out[r, c] = bf16(A[r, c] * s[c]) (or / s[c]); a 1-D tensor is one row. ``out=A`` works in place."""
@@ -393,7 +393,7 @@ def scale_columns(A: torch.Tensor, s: torch.Tensor, divide: bool = False, out: t
     return out
 
 
-@_on_device
+@_on_first_device
 def scale_rows(A: torch.Tensor, s: torch.Tensor, divide: bool = False, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """out[r, c] = bf16(A[r, c] * s[r]) (or / s[r]); a 1-D tensor is scaled element-wise."""
@@ -429,7 +429,7 @@ def fold_linear_linear(w1: torch.Tensor, b1: torch.Tensor | None, w2: torch.Tens
 
 
 # --------------------------------------------------------------------------------------------- (7)
-@_on_device
+@_on_first_device
 def w4a16_gemm(X: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, zeros: torch.Tensor,
                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X' deq(W)^T (bf16 [M, O]) from packed codes [O, K/8], steps and zeros [O, K/128]."""
