@@ -16,7 +16,7 @@ def _sums(X, steps, zeros):
 def few(X, codes, steps, zeros):
     """(X deq(W)^T in 64 bits, bound of the few-token kernel before its output rounding), in units of 2^-24. Per group, S sums q x
     by 8 MMAs of 16 products and the sum so far; each of the 17 may be cut by 2 units of the largest, at most 15 A; the same for
-    the sum of x, times |z|. x in fp16 is off by 2^-35 of the group's largest, less than one unit of (15 + |z|) A. Then a
+    the sum of x, times |z|. x in fp16 is off by 2^-39 of the group's largest, less than one unit of (15 + |z|) A. Then a
     rounding of (15 + |z|) A each for z's product and the step's, and one per sum over G groups and 8 slices."""
     A, step, z = _sums(X, steps, zeros)
     G = steps.shape[1]

@@ -181,3 +181,24 @@ def test_rows_of_experts_with_wild_steps_and_zero_points():
     X = normal((rows, K), 191)
     got = awq.w4a16_experts(X.cuda(), offsets_of([rows]).cuda(), *(t[None].cuda() for t in W))
     plain.assert_within(got, *bounds.grouped(X, *W))
+
+
+@pytest.mark.parametrize("K", [1024, 28672])
+@pytest.mark.parametrize("kind", ["centred", "outliers", "one-sided", "squared"])
+def test_few_tokens_sum_as_fp32_does(K, kind):
+    """With minus the result as the bias, the output is what the result's rounding to bf16 left, r, and the error of the sums: seen
+    to 2^-9 of r. The sums may be off by 2^-17 of the result's norm: cut to fp32 at every MMA without a guard bit they are by
+    4e-6 at K = 28672. Activations around zero, with channels twenty times as large, of one sign, and squared."""
+    M, O = 4, 1024
+    X = torch.randn(M, K, generator=torch.Generator().manual_seed(200))
+    if kind == "outliers":
+        X[:, 7::200] *= 20
+    if kind in ("one-sided", "squared"):
+        X = X.clamp(min=0) if kind == "one-sided" else X.clamp(min=0) ** 2
+    X, W = X.bfloat16(), weights_around_zero(O, K, 201)
+    ref = X.double() @ plain.dequantized(*W).T
+    Wd, bias = tuple(t.cuda() for t in W), -ref.bfloat16()
+    left = ref + bias.double()
+    got = torch.cat([awq.w4a16_gemv(X[m:m + 1].cuda(), *Wd, bias=bias[m].cuda()) for m in range(M)])
+    off = float((got.double().cpu() - left).norm() / ref.norm())
+    assert off <= 2.0 ** -9 * float(left.norm() / ref.norm()) + 2.0 ** -17, off

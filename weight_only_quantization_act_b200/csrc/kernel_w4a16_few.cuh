@@ -5,13 +5,17 @@
 // Mathematics: per group g of 128 in-features and token m, with a power of two c[m, g] that brings the group's largest
 // |x'| to 2^14..2^15 and xs = c x',
 //   Y[m, o] = sum_g step[o, g] / c[m, g] (sum_{k in g} q[o, k] xs[m, k] - z[o, g] sum_{k in g} xs[m, k]).
-// A nibble in place in bits 0-3 of a half-word is the fp16 subnormal q 2^-24, in bits 4-7 q 2^-20, so one AND per two codes
-// and one shift per eight make the operand. xs of the in-features that meet the latter is stored as xs / 16, so every term
-// counts 2^-24, and the 2^24 goes into 1 / c. A bf16 x is exact in fp16 down to 2^-28 of its group's largest and below that
-// off by 2^-35 of it, so the weights enter with their exact value; the tensor cores sum 15 |xs| at most in fp32, the step
-// and zero point are applied once per group and output in fp32. (Nibbles under the exponent of 1024 or 64, 1024 + q, take as
-// many instructions, but their sums of 1024 xs have to be taken off again: for one-sided X, a ReLU's for one, up to 1e-2 of
-// the result was lost. bf16 patterns 128 + q need a shift for every pair of codes.)
+// A nibble in bits 4-7 of a half-word is the fp16 subnormal q 2^-20, so an AND and at most one shift per two codes make the
+// operand, and the 2^20 goes into 1 / c. A bf16 x is exact in fp16 down to 2^-31 of its group's largest and below that
+// off by 2^-39 of it, so the weights enter with their exact value; the tensor cores sum 15 |xs| at most in fp32, the step
+// and zero point are applied once per group and output in fp32.
+// The tensor cores line products up by the exponents of the operands as they are stored, 2^-14 for every subnormal, and cut
+// what is below fp32's last place there, so a nibble has to stand high. Measured error ahead of the output's rounding, of its
+// norm, 28672 in-features: 3e-6 at most for activations around zero, with outliers, of one sign and squared (2.4e-6 is
+// what the measurement resolves), as for the plain fp32 form. With nibbles in bits 0-3 and 4-7, one shift per eight codes,
+// 4e-4 for squared ones (and 34.8 us, not 36.9, for 28672 -> 8192), in bits 2-5 and 6-9 5e-5 (34.9), all in bits 6-9 5e-6 (37.0).
+// Nibbles under the exponent of 1024 or 64, 1024 + q, whose constants' sums have to be taken off again, 1.2e-3 (36.5).
+// (bf16 patterns 128 + q need a shift for every pair of codes.)
 //
 // The bound is HBM: a weight is read once and used for at most 8 tokens (0.5 byte per 16 operations), so
 // what matters is bytes in flight and few instructions per weight. A one-token product cannot fill the
@@ -134,11 +138,12 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-// Codes 0 and 4 of a word as fp16 numbers q 2^-24, codes 1 and 5 as q 2^-20. The other four: the same of w >> 8.
-__device__ __forceinline__ uint32_t code_even(uint32_t w) { return w & 0x000F000Fu; }
-__device__ __forceinline__ uint32_t code_odd(uint32_t w) { return w & 0x00F000F0u; }
-// Minus one in the same units.
-constexpr uint32_t MINUS_EVEN = 0x80018001u, MINUS_ODD = 0x80108010u;
+// Two codes of a word, n and n + 4, as fp16 numbers q 2^-20.
+template <int N>
+__device__ __forceinline__ uint32_t codes_of(uint32_t w) {
+  return (N == 0 ? w << 4 : w >> (4 * N - 4)) & 0x00F000F0u;
+}
+constexpr uint32_t MINUS_ONE = 0x80108010u;  // in the same units
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
   float* part = reinterpret_cast<float*>(smem);
   uint8_t* xs = smem + PART_BYTES;                                         // [group][word][token][t4] 16 bytes
   float2* param = reinterpret_cast<float2*>(xs + (p.xg * 256 << p.mp_log2));  // [group][PARAM_LD]: step, zero point
-  float2* sx = param + (p.xg * PARAM_LD + 1) / 2 * 2;  // [group][TOKENS]: -(sum of xs) 2^-24, 2^24 / c
+  float2* sx = param + (p.xg * PARAM_LD + 1) / 2 * 2;  // [group][TOKENS]: -(sum of xs) 2^-20, 2^20 / c
 
   const uint32_t* codes = p.codes + e * p.O * (p.K / 8) + g_begin * 16;
   const uint32_t* code[4];  // the lane's pieces of its rows g8, g8 + 8, g8 + 16, g8 + 24
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
   };
 
   // X of the tokens and of groups gc..gc+ng-1 as fp16, scaled and permuted so that one 16-byte piece (in-features
-  // 8w..8w+7) holds the pairs (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16. The 16 threads of a token's group are neighbours.
+  // 8w..8w+7) holds the pairs (0, 4), (1, 5), (2, 6), (3, 7). The 16 threads of a token's group are neighbours.
   auto stage_x = [&](int gc, int ng) {
     const int per_token = ng * 16;
     constexpr int AT_ONCE = 4;  // loads in flight per thread
@@ -236,21 +241,21 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
         uint32_t most = max(max(exponent_max(v[k].x), exponent_max(v[k].y)), max(exponent_max(v[k].z), exponent_max(v[k].w)));
 #pragma unroll
         for (int d = 1; d < 16; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-        // c = 2^(14 - exponent), below 2^127; 2^24 / c is a normal number up to an exponent of 117
+        // c = 2^(14 - exponent), below 2^127; 2^20 / c is a normal number up to an exponent of 121
         const uint32_t field = min(268u - (most >> 7), 253u);
-        const float scale = __uint_as_float(field << 23), odd = __uint_as_float((field - 4u) << 23);
+        const float scale = __uint_as_float(field << 23);
         __half2 h[4];
         h[0] = __floats2half2_rn(bf16_lo(v[k].x) * scale, bf16_lo(v[k].z) * scale);
-        h[1] = __floats2half2_rn(bf16_hi(v[k].x) * odd, bf16_hi(v[k].z) * odd);
+        h[1] = __floats2half2_rn(bf16_hi(v[k].x) * scale, bf16_hi(v[k].z) * scale);
         h[2] = __floats2half2_rn(bf16_lo(v[k].y) * scale, bf16_lo(v[k].w) * scale);
-        h[3] = __floats2half2_rn(bf16_hi(v[k].y) * odd, bf16_hi(v[k].w) * odd);
+        h[3] = __floats2half2_rn(bf16_hi(v[k].y) * scale, bf16_hi(v[k].w) * scale);
         if (to[k] >= 0) {
           const int mk = to[k] >> 16, ck = to[k] & 0xFFFF;
           const int grp = ck >> 4, t = (ck >> 2) & 3, word = ck & 3;
           *reinterpret_cast<uint4*>(xs + (((grp * 4 + word) * mp + mk) * 4 + t) * 16) = *reinterpret_cast<const uint4*>(h);
           if ((ck & 15) == 0) {
-            sx[grp * TOKENS + mk].y = __uint_as_float(min(278u - field, 254u) << 23);
-            if (field < 24u) atomicOr(&apart, 1u << mk);  // 2^118 and more, infinities, NaN
+            sx[grp * TOKENS + mk].y = __uint_as_float(min(274u - field, 254u) << 23);
+            if (field < 20u) atomicOr(&apart, 1u << mk);  // 2^122 and more, infinities, NaN
           }
         }
       }
@@ -272,9 +277,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
       float s[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (k == 0) mma16816_first(s, MINUS_EVEN, MINUS_EVEN, MINUS_ODD, MINUS_ODD, x[k].x, x[k].y);
-        else mma16816(s, MINUS_EVEN, MINUS_EVEN, MINUS_ODD, MINUS_ODD, x[k].x, x[k].y);
-        mma16816(s, MINUS_EVEN, MINUS_EVEN, MINUS_ODD, MINUS_ODD, x[k].z, x[k].w);
+        if (k == 0) mma16816_first(s, MINUS_ONE, MINUS_ONE, MINUS_ONE, MINUS_ONE, x[k].x, x[k].y);
+        else mma16816(s, MINUS_ONE, MINUS_ONE, MINUS_ONE, MINUS_ONE, x[k].x, x[k].y);
+        mma16816(s, MINUS_ONE, MINUS_ONE, MINUS_ONE, MINUS_ONE, x[k].z, x[k].w);
       }
       if (g8 == 0) {  // the rows of the result are all the same
         sx[gx * TOKENS + 2 * t4].x = s[0];
@@ -334,12 +339,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t lo = word_of(w[d][2 * i], k), hi = word_of(w[d][2 * i + 1], k);
-            const uint32_t l8 = lo >> 8, h8 = hi >> 8;
             if (k == 0)
-              mma16816_first(s[i], code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
+              mma16816_first(s[i], codes_of<0>(lo), codes_of<0>(hi), codes_of<1>(lo), codes_of<1>(hi), x[k].x, x[k].y);
             else
-              mma16816(s[i], code_even(lo), code_even(hi), code_odd(lo), code_odd(hi), x[k].x, x[k].y);
-            mma16816(s[i], code_even(l8), code_even(h8), code_odd(l8), code_odd(h8), x[k].z, x[k].w);
+              mma16816(s[i], codes_of<0>(lo), codes_of<0>(hi), codes_of<1>(lo), codes_of<1>(hi), x[k].x, x[k].y);
+            mma16816(s[i], codes_of<2>(lo), codes_of<2>(hi), codes_of<3>(lo), codes_of<3>(hi), x[k].z, x[k].w);
           }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) w4a16_few_kernel(const P
     mine[(2 * t4 + 1) * PART_LD + 8] = acc[i][3];
   }
   // What the group sums cannot give, since they take z sum x off sum q x: tokens with an infinity or a NaN again (or with a
-  // value of 2^118 and more, whose 2^24 / c is no number), term by term from the weights as fp32 numbers, so that each
+  // value of 2^122 and more, whose 2^20 / c is no number), term by term from the weights as fp32 numbers, so that each
   // output is the infinity or the NaN of the definition (as in the experts' grouped kernel). A column of the MMA is a token,
   // so the others have not been touched.
   const unsigned tokens_apart = apart;
