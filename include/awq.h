@@ -360,14 +360,16 @@ AWQ_API awq_status awq_expert_combine_backward(const void *dY, int64_t T, int64_
  * Products of the experts (W4A16): Y[r] = Xs[r] deq(W_e)^T for the rows offsets[e] <= r < offsets[e + 1] of
  * every expert e, or with gated = 1 the gated form of awq_w4a16_gemv. The weights enter with
  * their exact value, (q - z) summed per group and scaled by the fp32 step; only in a group with |z| > 240 (its
- * weights nearly equal) an expert with more than 8 rows takes q - z rounded to bf16.
+ * weights nearly equal) an expert with more than 8 rows takes q - z rounded to bf16. zeros must be whole numbers, as packing
+ * gives them: with more than 8 rows another z enters rounded to bf16.
  *   Xs      device bf16 [R, K] sorted rows, row stride ldx (multiple of 8)
  *   codes   device uint32 [E, O, K/8], 16-byte aligned; steps / zeros device float [E, O, K/128] (as packed:
  *           integer-valued zeros)
  *   Y       device bf16 [R, O] (gated: [R, O/2]), row stride ldy >= its columns; rows from offsets[E] on are left
  *           as they were; must not overlap Xs
  *   workspace  device, 16-byte aligned, >= awq_w4a16_experts_workspace_size(R, E, K, O) bytes, ZERO-FILLED
- *           BEFORE ITS FIRST USE and after a device timeout, which awq_search_status() reports on it
+ *           BEFORE ITS FIRST USE and after a device timeout, which awq_search_status() reports on it: rows of
+ *           experts with more than 8 rows may then be left as they were, in that call and until it is zeroed
  * Requires K % 128 == 0, any O >= 1 (gated: even), 1 <= E <= AWQ_MAX_EXPERTS. Deterministic.
  * ------------------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_w4a16_experts_workspace_size(int64_t R, int64_t E, int64_t K, int64_t O);

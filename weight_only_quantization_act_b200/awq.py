@@ -704,7 +704,7 @@ def w4a16_experts(Xs: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor, 
                   gated: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                   *, stream=None) -> torch.Tensor:
     """Products of sorted rows with their experts' packed weights: Y[r] = Xs[r] deq(W_e)^T for offsets[e] <= r <
-    offsets[e + 1] (codes [E, O, K/8], steps and zeros [E, O, K/128]); ``gated`` as in w4a16_gemv. Rows behind the last
+    offsets[e + 1] (codes [E, O, K/8], steps and whole-numbered zeros [E, O, K/128]); ``gated`` as in w4a16_gemv. Rows behind the last
     routed one are not written.
 
     A device wait that gives up (set_wait_limit_ns) leaves rows of experts with more than 8 rows as they were and its status in the

@@ -19,8 +19,8 @@
 // expert's last row.
 //
 // Bounds: at N = 192 a group takes the tensor cores 768 cycles, the unpacking about 200 and the scaling about 140
-// issue cycles of every SM quarter. Below N = 60 the codes arrive no faster than that from HBM (9 KB per SM and
-// group). 192 and not 256 tokens: two accumulators of N columns and two operand buffers of 64 fill tensor memory. Where
+// issue cycles of every SM quarter. Below N = 100 the codes arrive no faster than that from HBM (9 KB per SM and
+// group, 400 cycles at the 6.6 TB/s of a copy). 192 and not 256 tokens: two accumulators of N columns and two operand buffers of 64 fill tensor memory. Where
 // every tile of the call is narrower, three groups (up to 96 tokens) or four (up to 64) are in flight instead of two: the
 // way from a group's end through the unpackers and scaling warps to the next group's MMAs takes about 2000 cycles.
 //
@@ -37,16 +37,17 @@
 // The thread that issues the MMAs waits once per group: one barrier counts the token rows, the unpacked operand and the
 // reading of the accumulator that the group will overwrite, and one commit per group tells all three that it is done
 // (with a wait and a commit for each, and per 64 in-features, that thread took 1700 cycles per group). Every wait
-// is bounded.
+// is bounded, and one that gives up ends its role.
 //
-// Measured (B200): 16384 rows to 32 experts of 4096 -> 2 x 2048, gated, 553 us, 1.0 PFLOP/s; 600 rows to 8 of
-// 14336 -> 4096 155 us; 96 rows to 8 of 4096 -> 2 x 14336, gated, 221 us. Two things bound it. A group's work is short
-// against what surrounds it: the barriers alone, with neither unpacking, scaling, loads nor more than one MMA, take 700
-// cycles per group, and what counted most was every instruction in the loops of the unpackers and scaling warps (a test
-// per block, the remote barrier's address made anew for each arrival, an unlikely branch before the stores and a poll
-// with a suspend time together cost 742 against 581 us for the 16384 rows; unpackers that share each group instead of
-// taking them in turn 581 against 553). And at 192 tokens the accumulators that fit are two, so the scaling of a group
-// has one group's MMAs to hide behind.
+// Measured (B200, calls back to back on a router's counts): 16384 rows to 32 experts of 4096 -> 2 x 2048, gated, 650 us, 0.85
+// PFLOP/s (the kernel by itself 638; 512 rows to each expert 589); 600 rows to 8 of 14336 -> 4096 150 to 161 us; 12 rows to
+// each of 8 of 4096 -> 2 x 14336, gated, 232 us, and the same for 9 to 64 rows each. Two things bound it. A group's work is
+// short against what surrounds it: the barriers alone, with neither unpacking, scaling, loads nor more than one MMA, take 700
+// cycles per group, and what counted most was every instruction in the loops of the unpackers and scaling warps (for the
+// 16384 rows, where the kernel stood at 553 us in a probe: a test per block, the remote barrier's address made anew for each
+// arrival, an unlikely branch before the stores and a poll with a suspend time together 742 against 581; unpackers that share
+// each group instead of taking them in turn 581 against 553). And at 192 tokens the accumulators that fit are two, so the
+// scaling of a group has one group's MMAs to hide behind.
 #pragma once
 #include <cstdint>
 #include <type_traits>

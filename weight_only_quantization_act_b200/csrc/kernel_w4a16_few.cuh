@@ -33,12 +33,16 @@
 // add their fp32 partial sums through distributed shared memory in slice order: one launch, no workspace, the same
 // result every time.
 //
-// Measured (B200, weights of one token and of 8 experts with 2 rows each): 28672 -> 8192 in 32 us in a graph and
-// 8 x (4096 -> 2 x 14336) in 135 us by itself, 4.1 and 3.9 TB/s of packed weights. What bounds it is how many loads the SM
-// keeps in flight and how they fall on DRAM pages, then the instructions between them: with one group ahead and 4 CTAs per SM
-// 36 and 201 us, with three ahead and 4 CTAs (which spills, and opens more rows at once) 36 and 235, with seven ahead and 2
-// CTAs 35 and 163, with four ahead 32 and 143; with a bulk prefetch of each row into L2 instead 36 and 201; with a predicate
-// per load of X and addresses made per group 33 and 142; without the loads, the rest took 25 and 108.
+// Measured (B200, weights that no cache holds): 28672 -> 8192 for one token in 35.4 us in a graph and 37.6 as calls, for 8
+// tokens 49 and 51 (w4a16_gemm 50.4 and 52.3, 51 and 53); 4096 -> 4096 8.0 and 10.9 (10.6 and 17.2); 5 tokens 4224 -> 2 x
+// 10756, gated, 23.9 and 25.7; 8 experts of 4096 -> 2 x 14336, gated, with 1, 2, 4 and 8 rows each 118, 126, 139 and 168 us
+// back to back. That is 3.7 and, with 2 rows, 4.2 TB/s of packed weights. Without the loads of the codes the rest takes
+// 29.6 us of the 35.4 and 105 of the 126, so it is bound twice: by the instructions of a group, and by how many loads the SM
+// keeps in flight and how they fall on DRAM pages.
+// Layouts, measured before the nibbles moved to bits 4-7, on the same weights again and again, 32 us for 28672 -> 8192 in a
+// graph and 135 for 2 rows to each of 8 experts: one group ahead and 4 CTAs per SM 36 and 201 us, three ahead and 4 CTAs
+// (which spills, and opens more rows at once) 36 and 235, seven ahead and 2 CTAs 35 and 163, four ahead 32 and 143; a bulk
+// prefetch of each row into L2 instead 36 and 201; a predicate per load of X and addresses made per group 33 and 142.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -66,9 +70,9 @@ __host__ __device__ constexpr int smem_bytes(int xg, int mp) {
   return PART_BYTES + xg * 256 * mp + (xg * PARAM_LD + 1) / 2 * 16 + xg * TOKENS * 8;
 }
 // The most groups that fit: what precedes a chunk's first group (its X, steps and zero points on their way, the sums of X)
-// leaves the loads of the codes with the three groups ahead, so few, long and equal chunks
-// (17 groups of 5 tokens as one chunk of 20 and not 16 + 1: 20.6 to 19.7 us). With 74 KB per CTA the L1 that remains holds too few
-// loads: 28672 -> 8192 for 8 tokens 46 to 55 us.
+// leaves the loads of the codes with the three groups ahead, so few and long chunks, as equal as DEPTH lets them be. With 67 KB
+// per CTA the L1 that remains holds too few loads: 28672 -> 8192 for 8 tokens 49 to 58 us, 5 gated tokens 4224 -> 2 x 10756
+// 24 to 33.
 __host__ __device__ constexpr int chunk_groups(int mp) {
   return (CHUNK_BYTES - PART_BYTES) / (256 * mp + 8 * PARAM_LD + TOKENS * 8) / DEPTH * DEPTH;
 }

@@ -249,8 +249,10 @@ __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
 // RN32(r (1 + 2^-22)) enclose 1 / s, so RN32(x r-) and RN32(x r+) enclose RN32(x / s) (rounding keeps order), and where both
 // round to the same bf16 that is the result. Where they do not, the division decides. (8 divisions per 16 bytes, or a test of
 // every quotient's low bits, took twice the time that the rows take from HBM.)
-// Measured (B200): 65536 rows of 4096 columns for 128 experts with the sort in 128 us, 4.4 TB/s, bound by instruction issue: with
-// a row's address and expert made by every thread 161, with 8 rows in flight (96 registers) 181, runs of 64 rows the same.
+// Measured (B200): 65536 rows of 4096 columns for 128 experts with the sort in 128 us, 4.4 TB/s; this kernel 113, with 57 % of
+// DRAM's rate and 2.1 of 4 instructions per cycle, so bound by neither: its warps (40 % of what an SM holds) wait for their
+// loads. With a row's address and expert made by every thread 161, with 8 rows in flight (96 registers) 181, runs of 64
+// rows the same.
 constexpr int RUN = 32;
 __global__ void __launch_bounds__(ROW_THREADS) expert_gather_scaled_kernel(
     const uint16_t* __restrict__ X, int64_t ldx, int64_t T, int64_t K, const int* __restrict__ offsets, int E,
