@@ -20,9 +20,10 @@
 //
 // Bounds: at N = 192 a group takes the tensor cores 768 cycles, the unpacking about 200 and the scaling about 140
 // issue cycles of every SM quarter. Below N = 100 the codes arrive no faster than that from HBM (9 KB per SM and
-// group, 400 cycles at the 6.6 TB/s of a copy). 192 and not 256 tokens: two accumulators of N columns and two operand buffers of 64 fill tensor memory. Where
-// every tile of the call is narrower, three groups (up to 96 tokens) or four (up to 64) are in flight instead of two: the
-// way from a group's end through the unpackers and scaling warps to the next group's MMAs takes about 2000 cycles.
+// group, 400 cycles at the 6.6 TB/s of a copy). 192 and not 256 tokens: two accumulators of N columns and two operand
+// buffers of 64 fill tensor memory. Where every tile of the call is narrower, three groups (up to 96 tokens) or four (up to
+// 64) are in flight instead of two: the way from a group's end through the unpackers and scaling warps to the next group's
+// MMAs takes about 2000 cycles.
 //
 // Persistent, clusters of 2 CTAs, one CTA per SM; every CTA makes the table of tiles from the row offsets for
 // itself and takes each n-th tile, so nothing is exchanged between pairs. Warps of a CTA:
@@ -211,8 +212,8 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, DeviceS
   }
   return true;
 }
-// For one thread. Where all lanes of a warp poll, what lane 0 has seen counts: after a __syncwarp the phase is complete for the
-// others too, also for one that has given up.
+// For one thread. Where all lanes of a warp poll, lane 0 arrives for them if it has not given up itself: the phase is then
+// complete, also for a lane that has, whose own reading may have come too early and which discards the tile.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Params& p, unsigned where) {
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, p.status, p.limit_ns, where);
 }
@@ -566,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t c_first = c_tile(0) + C_BYTES + static_cast<uint32_t>(r * 8);
     const uint32_t ta0 = tmem_base + static_cast<uint32_t>(half * BLOCK) + (static_cast<uint32_t>(quarter * 32) << 16);
     uint32_t phase = 0, i = 0, buf = 0, ct = c_first, ta = ta0;
-    int who = lane;  // the lane with 0 here arrives for the warp; -1 where it has given up
+    int who = lane;  // the lane with 0 here arrives for the warp; -1 in a lane that has given up
     if (lane == 0)  // every accumulator is free
       for (uint32_t d = 0; d < depth; ++d) mbar_arrive_pair(map_to_rank(full_bar(d), 0));
     for (int t = pair; t < num_tiles && warp_ok(st); t += n_pairs) {
@@ -622,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (mine >= 3) scale_groups(std::integral_constant<int, 3>{});
       else if (mine == 2) scale_groups(std::integral_constant<int, 2>{});
       else scale_groups(std::integral_constant<int, 1>{});
-      if (!__any_sync(0xffffffffu, who == 0)) break;  // nothing of an unfinished tile is stored
+      if (__any_sync(0xffffffffu, who < 0)) break;  // nothing of an unfinished tile is stored
 
       int64_t o, n_out;
       if (GATED) {
